@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libmoe_fp8.so")
 
 MOE_BF16, MOE_F32 = 0, 1
 MOE_EPI_BF16, MOE_EPI_SWIGLU_FP8, MOE_EPI_F32 = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
+MOE_B_NK, MOE_B_KN = 0, 1
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_ALIGN",
           4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_DEVICE", 6: "MOE_ERR_UNSUPPORTED",
@@ -61,6 +63,44 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _LL = ctypes.c_longlong
+_F = ctypes.c_float
+_SZ = ctypes.c_size_t
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [("T", _I), ("H", _I), ("x_dtype", _I), ("b_dtype", _I),
+                ("x", _P), ("ldx", _LL), ("b", _P), ("ldb", _LL), ("w_pre", _P), ("w_post", _P),
+                ("gate_mode", _I), ("gate", _P), ("ldg", _LL),
+                ("alpha", _F), ("beta", _F), ("eps", _F),
+                ("r", _P), ("ldr", _LL), ("h", _P), ("ldh", _LL)]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [("T", _I), ("H", _I), ("x_dtype", _I), ("b_dtype", _I),
+                ("r", _P), ("ldr", _LL), ("dr", _P), ("lddr", _LL), ("dh", _P), ("lddh", _LL),
+                ("b", _P), ("ldb", _LL), ("w_pre", _P), ("w_post", _P),
+                ("gate_mode", _I), ("gate", _P), ("ldg", _LL),
+                ("alpha", _F), ("beta", _F), ("eps", _F),
+                ("dx", _P), ("lddx", _LL), ("db", _P), ("lddb", _LL),
+                ("dw_pre", _P), ("dw_post", _P), ("dgate", _P), ("lddg", _LL)]
+
+
+class GemmBf16Args(ctypes.Structure):
+    _fields_ = [("a", _P), ("lda", _LL), ("a_rows", _I), ("a_row_index", _P), ("b", _P),
+                ("b_layout", _I), ("group_offsets", _P), ("num_groups", _I), ("total_rows", _I),
+                ("n_out", _I), ("k_dim", _I), ("out_dtype", _I), ("out", _P), ("ldo", _LL),
+                ("row_scale", _P)]
+
+
+class WgradBf16Args(ctypes.Structure):
+    _fields_ = [("a", _P), ("lda", _LL), ("a_rows", _I), ("a_row_index", _P),
+                ("b", _P), ("ldb", _LL), ("b_rows", _I), ("b_row_index", _P),
+                ("group_offsets", _P), ("num_groups", _I), ("total_rows", _I), ("n", _I),
+                ("k", _I), ("out_dtype", _I), ("out", _P), ("accumulate", _I)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("src", _P), ("dst", _P), ("numel", _LL), ("src_dtype", _I), ("dst_dtype", _I)]
 
 
 def lib():
@@ -92,6 +132,16 @@ def lib():
             "moe_probe_hbm": [_I, _P, ctypes.c_size_t, _P, _P],
             "moe_permute_noalloc": [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P],
             "moe_layer_forward": [ctypes.POINTER(LayerArgs), _P, ctypes.c_size_t, _P],
+            "moe_block_norm": [ctypes.POINTER(BlockNormArgs), _P],
+            "moe_block_norm_backward": [ctypes.POINTER(BlockNormBwdArgs), _P, _SZ, _P],
+            "moe_grouped_gemm_bf16": [ctypes.POINTER(GemmBf16Args), _P],
+            "moe_grouped_wgrad_bf16": [ctypes.POINTER(WgradBf16Args), _P, _SZ, _P],
+            "moe_swiglu": [_P, _I, _I, _I, _LL, _P, _LL, _P],
+            "moe_swiglu_backward": [_P, _P, _I, _I, _I, _LL, _LL, _P, _P, _LL, _P, _P, _LL, _P],
+            "moe_grad_table": [ctypes.POINTER(GradTensor), _I, _P, _SZ, ctypes.POINTER(_LL)],
+            "moe_grad_norm": [_P, _I, _LL, _P, _SZ, _P, _P, _P],
+            "moe_grad_scale": [_P, _I, _LL, _P, _F, _P, _P],
+            "moe_grad_clip": [_P, _I, _LL, _P, _SZ, _F, _P, _P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -105,6 +155,14 @@ def lib():
         L.moe_permute_noalloc_max_scratch_bytes.restype = ctypes.c_size_t
         L.moe_layer_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I]
         L.moe_layer_workspace_bytes.restype = ctypes.c_size_t
+        L.moe_block_norm_backward_workspace_bytes.argtypes = [_I, _I]
+        L.moe_block_norm_backward_workspace_bytes.restype = _SZ
+        L.moe_grouped_wgrad_bf16_workspace_bytes.argtypes = [_I, _I, _I, _I]
+        L.moe_grouped_wgrad_bf16_workspace_bytes.restype = _SZ
+        L.moe_grad_table_bytes.argtypes = [_I]
+        L.moe_grad_table_bytes.restype = _SZ
+        L.moe_grad_norm_workspace_bytes.argtypes = [_LL]
+        L.moe_grad_norm_workspace_bytes.restype = _SZ
         L.moe_status_str.argtypes = [_I]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_last_hip_error.argtypes = []
@@ -499,6 +557,312 @@ def moe_layer_forward(w, x, k, gamma=1e-3, n_groups=1, topk_groups=1, router_fp8
     _check("moe_layer_forward", lib().moe_layer_forward(ctypes.byref(a), _ptr(ws), ws.numel(),
                                                         _stream(stream)))
     return y
+
+
+# ---------------------------------------------------------------------------
+# training in bf16: the norms around the block, the experts' products, the
+# activation between them, and clipping
+
+
+_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _dtype_code(t, name):
+    if t.dtype not in _DT:
+        raise ValueError(f"{name}: need bfloat16 or float32, got {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _rows(t, shape, dtype, name):
+    """A device matrix whose rows are contiguous; returns (pointer, row stride)."""
+    if t is None:
+        return None, 0
+    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape)
+            and (t.stride(1) == 1 or t.shape[1] <= 1)):
+        raise ValueError(f"{name}: need a {dtype} device tensor {tuple(shape)} with contiguous "
+                         f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, n, name, dtype=torch.float32):
+    if t is None:
+        return None
+    if not (t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous()):
+        raise ValueError(f"{name}: need {n} contiguous {dtype} values on the device, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _gate(gate, T, H, b_dtype):
+    """(mode, pointer, row stride) of a gate [H], [T,1] or [T,H]."""
+    if gate is None:
+        return MOE_GATE_NONE, None, 0
+    if gate.dim() == 1:
+        return MOE_GATE_CHANNEL, _vector(gate, H, "gate"), 0
+    if tuple(gate.shape) == (T, 1):
+        return MOE_GATE_TOKEN, _vector(gate, T, "gate"), 0
+    return (MOE_GATE_FULL, *_rows(gate, (T, H), b_dtype, "gate"))
+
+
+def moe_block_norm(x, b=None, w_pre=None, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
+                   r=None, h=None, stream=None):
+    """The norms around a block with its gate and the residual scale:
+    r = alpha x + beta gate rmsnorm(b, w_post) and h = rmsnorm(r, w_pre).
+    x [T,H] the residual stream, b [T,H] the block's output (None: r is x),
+    w_pre / w_post float32 [H] (None: h is not formed / b is not normalised),
+    gate float32 [H] or [T,1], or [T,H] of b's type.  Returns (r, h); h has
+    b's type (x's without b) unless an output is given."""
+    T, H = x.shape
+    xdt = _dtype_code(x, "x")
+    if b is not None:
+        bt = b.dtype
+        _dtype_code(b, "b")
+        r = torch.empty(T, H, dtype=x.dtype, device=x.device) if r is None else r
+    else:
+        if gate is not None or w_post is not None:
+            raise ValueError("gate and w_post belong to a block output b")
+        bt = h.dtype if h is not None else x.dtype
+        r = None
+    if h is None and w_pre is not None:
+        h = torch.empty(T, H, dtype=bt, device=x.device)
+    mode, gp, ldg = _gate(gate, T, H, bt)
+    a = BlockNormArgs(T, H, xdt, _DT.get(bt, -1), *_rows(x, (T, H), x.dtype, "x"),
+                      *_rows(b, (T, H), bt, "b"), _vector(w_pre, H, "w_pre"),
+                      _vector(w_post, H, "w_post"), mode, gp, ldg, alpha, beta, eps,
+                      *_rows(r, (T, H), x.dtype, "r"), *_rows(h, (T, H), bt, "h"))
+    _check("moe_block_norm", lib().moe_block_norm(ctypes.byref(a), _stream(stream)))
+    return (x if b is None else r), h
+
+
+def moe_block_norm_backward_workspace_bytes(T, H):
+    return int(lib().moe_block_norm_backward_workspace_bytes(T, H))
+
+
+def moe_block_norm_backward(r, dr=None, dh=None, b=None, w_pre=None, w_post=None, gate=None,
+                            alpha=1.0, beta=1.0, eps=1e-6, dx=None, db=None, dw_pre=None,
+                            dw_post=None, dgate=None, ws=None, stream=None):
+    """Backward of moe_block_norm from r (x when there was no b) and b, given
+    dr (r's other use) and dh, either of them None.  Returns (dx, db, dw_pre,
+    dw_post, dgate), None where the forward pass had no such input; the
+    weights' gradients and those of a [H] or [T,1] gate are float32."""
+    T, H = r.shape
+    dev = r.device
+    bt = b.dtype if b is not None else (dh.dtype if dh is not None else r.dtype)
+    mode, gp, ldg = _gate(gate, T, H, bt)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx = torch.empty(T, H, dtype=r.dtype, device=dev) if dx is None else dx
+    if b is not None:
+        db = torch.empty(T, H, dtype=bt, device=dev) if db is None else db
+        if w_post is not None and dw_post is None:
+            dw_post = torch.empty(H, **f32)
+        if mode == MOE_GATE_FULL:
+            dgate = torch.empty(T, H, dtype=bt, device=dev) if dgate is None else dgate
+        elif mode != MOE_GATE_NONE:
+            dgate = torch.empty(gate.shape, **f32) if dgate is None else dgate
+    elif gate is not None or w_post is not None:
+        raise ValueError("gate and w_post belong to a block output b")
+    if dh is not None and w_pre is None:
+        raise ValueError("dh needs w_pre")
+    if dh is not None and dw_pre is None:
+        dw_pre = torch.empty(H, **f32)
+    if ws is None:
+        ws = torch.empty(max(moe_block_norm_backward_workspace_bytes(T, H), 16), dtype=torch.uint8,
+                         device=dev)
+    if mode == MOE_GATE_FULL:
+        dgp, lddg = _rows(dgate, (T, H), bt, "dgate")
+    else:
+        dgp, lddg = _vector(dgate, H if mode == MOE_GATE_CHANNEL else T, "dgate"), 0
+    a = BlockNormBwdArgs(T, H, _dtype_code(r, "r"), _DT.get(bt, -1), *_rows(r, (T, H), r.dtype, "r"),
+                         *_rows(dr, (T, H), r.dtype, "dr"), *_rows(dh, (T, H), bt, "dh"),
+                         *_rows(b, (T, H), bt, "b"), _vector(w_pre, H, "w_pre"),
+                         _vector(w_post, H, "w_post"), mode, gp, ldg, alpha, beta, eps,
+                         *_rows(dx, (T, H), r.dtype, "dx"), *_rows(db, (T, H), bt, "db"),
+                         _vector(dw_pre, H, "dw_pre"), _vector(dw_post, H, "dw_post"), dgp, lddg)
+    _check("moe_block_norm_backward", lib().moe_block_norm_backward(
+        ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)))
+    return dx, db, dw_pre, dw_post, dgate
+
+
+def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_index=None,
+                          row_scale=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Grouped bf16 product: out[r] = row_scale[r] * A[src(r)] @ B[g]^T for the
+    rows r of each group, b bf16 [G, n_out, K]; with b_kn, A[src(r)] @ B[g], b
+    [G, K, n_out] (the input gradient, from the forward product's weights).
+    a bf16 [rows, K] (rows contiguous), group_offsets int32 [G+1] on the
+    device.  Returns out [total_rows, n_out] bf16 or float32."""
+    G = b.shape[0]
+    K, n = (b.shape[1], b.shape[2]) if b_kn else (b.shape[2], b.shape[1])
+    _dev(b, torch.bfloat16, "b"), _dev(group_offsets, torch.int32, "group_offsets")
+    if group_offsets.numel() != G + 1:
+        raise ValueError(f"group_offsets: need {G + 1} values")
+    if out is None:
+        out = torch.empty(total_rows, n, dtype=out_dtype, device=a.device)
+    ap, lda = _rows(a, (a.shape[0], K), torch.bfloat16, "a")
+    op, ldo = _rows(out, (total_rows, n), out.dtype, "out")
+    args = GemmBf16Args(ap, lda, a.shape[0],
+                        _vector(a_row_index, total_rows, "a_row_index", torch.int32),
+                        b.data_ptr(), MOE_B_KN if b_kn else MOE_B_NK, group_offsets.data_ptr(), G,
+                        total_rows, n, K, _dtype_code(out, "out"), op, ldo,
+                        _vector(row_scale, total_rows, "row_scale"))
+    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(ctypes.byref(args), _stream(stream)))
+    return out
+
+
+def moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k):
+    return int(lib().moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k))
+
+
+def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_row_index=None,
+                           accumulate=False, out=None, out_dtype=torch.float32, ws=None,
+                           stream=None):
+    """Weight gradients: out[g] = A_g^T B_g over the rows of each group, a bf16
+    [rows, n] (the output channels' gradient), b bf16 [rows, k] (the product's
+    input), each optionally gathered by its row index.  With accumulate it is
+    added to out.  Returns out [G, n, k] float32 or bf16."""
+    n, k = a.shape[1], b.shape[1]
+    _dev(group_offsets, torch.int32, "group_offsets")
+    G = group_offsets.numel() - 1
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty(G, n, k, dtype=out_dtype, device=a.device)
+    if tuple(out.shape) != (G, n, k):
+        raise ValueError(f"out: need [{G}, {n}, {k}], got {tuple(out.shape)}")
+    _dev(out, out.dtype, "out")
+    ap, lda = _rows(a, (a.shape[0], n), torch.bfloat16, "a")
+    bp, ldb = _rows(b, (b.shape[0], k), torch.bfloat16, "b")
+    need = moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+    args = WgradBf16Args(ap, lda, a.shape[0],
+                         _vector(a_row_index, total_rows, "a_row_index", torch.int32),
+                         bp, ldb, b.shape[0],
+                         _vector(b_row_index, total_rows, "b_row_index", torch.int32),
+                         group_offsets.data_ptr(), G, total_rows, n, k, _dtype_code(out, "out"),
+                         out.data_ptr(), 1 if accumulate else 0)
+    _check("moe_grouped_wgrad_bf16", lib().moe_grouped_wgrad_bf16(
+        ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+    return out
+
+
+def moe_swiglu(a, h=None, stream=None):
+    """h = silu(a[:, :I]) * a[:, I:] for rows a [R, 2I], bf16 or float32."""
+    R, I = a.shape[0], a.shape[1] // 2
+    if a.shape[1] % 2:
+        raise ValueError("a: need an even number of columns (gate columns, then up columns)")
+    h = torch.empty(R, I, dtype=a.dtype, device=a.device) if h is None else h
+    ap, lda = _rows(a, (R, 2 * I), a.dtype, "a")
+    hp, ldh = _rows(h, (R, I), a.dtype, "h")
+    _check("moe_swiglu", lib().moe_swiglu(ap, _dtype_code(a, "a"), R, I, lda, hp, ldh,
+                                          _stream(stream)))
+    return h
+
+
+def moe_swiglu_backward(a, dh, row_gate=None, da=None, dgate=None, hg=None, stream=None):
+    """Backward of row_gate[r] * swiglu(a)[r]: a [R, 2I], dh [R, I] the gradient
+    of the expert row before its gate, row_gate float32 [R] or None (all 1).
+    Returns (da [R, 2I], dgate float32 [R], hg [R, I] = row_gate * swiglu(a),
+    the second weight gradient's operand); pass dgate=False or hg=False for a
+    result that is not wanted."""
+    R, I = dh.shape
+    dt = _dtype_code(a, "a")
+    da = torch.empty(R, 2 * I, dtype=a.dtype, device=a.device) if da is None else da
+    dgate = torch.empty(R, dtype=torch.float32, device=a.device) if dgate is None else dgate
+    hg = torch.empty(R, I, dtype=a.dtype, device=a.device) if hg is None else hg
+    dgate, hg = (None if t is False else t for t in (dgate, hg))
+    ap, lda = _rows(a, (R, 2 * I), a.dtype, "a")
+    dhp, lddh = _rows(dh, (R, I), a.dtype, "dh")
+    dap, ldda = _rows(da, (R, 2 * I), a.dtype, "da")
+    hgp, ldhg = _rows(hg, (R, I), a.dtype, "hg")
+    _check("moe_swiglu_backward", lib().moe_swiglu_backward(
+        ap, dhp, dt, R, I, lda, lddh, _vector(row_gate, R, "row_gate"), dap, ldda,
+        _vector(dgate, R, "dgate"), hgp, ldhg, _stream(stream)))
+    return da, dgate, hg
+
+
+def _dense(t):
+    """Whether the tensor's elements fill one stretch of memory, in any order."""
+    if t.is_contiguous():
+        return True
+    order = sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1)
+    at = 1
+    for s, n in order:
+        if s != at:
+            return False
+        at *= n
+    return t.numel() > 0
+
+
+class GradList:
+    """The gradients of a model, for moe_grad_norm and moe_grad_clip: dense
+    device tensors, bf16 or float32, of any sizes (a permuted view counts as
+    dense).  outs: where the clipped gradients go, tensors of the same sizes
+    and strides (None: in place).  Built once; valid while the tensors keep
+    their memory, which this object holds on to.  Calls on one list share its
+    scratch: order them on one stream."""
+
+    def __init__(self, tensors, outs=None):
+        tensors = list(tensors)
+        outs = tensors if outs is None else list(outs)
+        if len(outs) != len(tensors):
+            raise ValueError("outs: need one tensor for every gradient")
+        if not tensors:
+            raise ValueError("tensors: need at least one gradient")
+        dev = tensors[0].device
+        for what, ts in (("tensors", tensors), ("outs", outs)):
+            for i, t in enumerate(ts):
+                _dtype_code(t, f"{what}[{i}]")
+                if not t.is_cuda or t.device != dev or not _dense(t):
+                    raise ValueError(f"{what}[{i}]: need a dense tensor on {dev}, got strides "
+                                     f"{t.stride()} on {t.device}")
+        for i, (s, d) in enumerate(zip(tensors, outs)):
+            if s.shape != d.shape or (s.stride() != d.stride() and not (s.is_contiguous()
+                                                                        and d.is_contiguous())):
+                raise ValueError(f"outs[{i}]: need the gradient's shape and strides")
+        self.tensors, self.outs, self.device = tensors, outs, dev
+        n = self.n = len(tensors)
+        rows = (GradTensor * n)(*[GradTensor(s.data_ptr(), d.data_ptr(), s.numel(), _DT[s.dtype],
+                                             _DT[d.dtype]) for s, d in zip(tensors, outs)])
+        host = torch.empty(lib().moe_grad_table_bytes(n), dtype=torch.uint8)
+        chunks = _LL(0)
+        _check("moe_grad_table", lib().moe_grad_table(rows, n, host.data_ptr(), host.numel(),
+                                                      ctypes.byref(chunks)))
+        self.chunks = chunks.value
+        self.table = host.to(dev)
+        self.ws = torch.empty(lib().moe_grad_norm_workspace_bytes(self.chunks), dtype=torch.uint8,
+                              device=dev)
+
+
+def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
+    """Global 2-norm of a GradList's gradients.  Returns (sumsq float64 [1],
+    norm float32 [1]), both on the device."""
+    sumsq = torch.empty(1, dtype=torch.float64, device=grads.device) if sumsq is None else sumsq
+    norm = torch.empty(1, dtype=torch.float32, device=grads.device) if norm is None else norm
+    _check("moe_grad_norm", lib().moe_grad_norm(
+        _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
+        _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), _stream(stream)))
+    return sumsq, norm
+
+
+def moe_grad_scale(grads, sumsq, max_norm, result=None, stream=None):
+    """The scaling of moe_grad_clip from a given sum of squares (float64 [1],
+    for instance summed over ranks).  Returns result float32 [2] (norm, coef)."""
+    result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
+    _check("moe_grad_scale", lib().moe_grad_scale(
+        _ptr(grads.table), grads.n, grads.chunks, _vector(sumsq, 1, "sumsq", torch.float64),
+        float(max_norm), _vector(result, 2, "result"), _stream(stream)))
+    return result
+
+
+def moe_grad_clip(grads, max_norm, result=None, stream=None):
+    """Clip a GradList to max_norm: outs = coef * gradients, coef = min(1,
+    max_norm / (norm + 1e-6)), or 1 when the norm is not finite.  Returns
+    result float32 [2] on the device: (norm, coef)."""
+    result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
+    _check("moe_grad_clip", lib().moe_grad_clip(
+        _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
+        float(max_norm), _vector(result, 2, "result"), _stream(stream)))
+    return result
 
 
 # ---------------------------------------------------------------------------

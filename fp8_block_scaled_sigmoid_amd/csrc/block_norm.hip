@@ -1,0 +1,472 @@
+// The norms around a block, fused with the block's gate and the residual
+// scale, and their backward pass.
+//
+// Forward, per token t (all sums and statistics in float):
+//   n = b / sqrt(mean(b^2) + eps) * w_post      (n = b without w_post)
+//   r = alpha x + beta gate n                   (r = x without a block output)
+//   h = r / sqrt(mean(r^2) + eps) * w_pre
+// Backward, with r^ = r / rms(r), b^ = b / rms(b) and d the gradient that
+// reaches r from both of its uses:
+//   v  = dh w_pre,   d  = dr + (v - r^ mean(v r^)) / rms(r),   dx = alpha d
+//   dn = beta gate d, u = dn w_post, db = (u - b^ mean(u b^)) / rms(b)
+//   dw_pre = sum_t dh r^,  dw_post = sum_t dn b^,  dgate = beta d n (summed
+//   over what the gate is shared by)
+// Both statistics come from the rows themselves, so nothing but r and b has to
+// be kept between the passes.
+#include "rows.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr int kMaxWaves = 16;
+constexpr int kMaxThreads = kMaxWaves * 64;
+constexpr int kMaxWidth = kMaxThreads * 16;   // two vectors of 8 a thread
+
+// How rows are laid over threads: `wpr` waves share a row, a workgroup holds
+// `groups` rows at a time, and a thread owns vectors t, t + 64 wpr of its row.
+struct RowShape {
+  int wpr, groups, items;
+};
+
+RowShape row_shape(int H) {
+  RowShape s;
+  const int vecs = (H + 7) / 8;
+  s.items = vecs > kMaxThreads ? 2 : 1;
+  s.wpr = (vecs + 64 * s.items - 1) / (64 * s.items);
+  s.groups = kMaxWaves / s.wpr;
+  return s;
+}
+
+// Sums N values over the waves of a row; every thread of the row gets them.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[kMaxWaves], int wave, int lane,
+                                         int first_wave, int wpr) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if (wpr == 1) return;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[i][wave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float t = 0.0f;
+    for (int w = 0; w < wpr; ++w) t += red[i][first_wave + w];
+    v[i] = t;
+  }
+}
+
+struct FwdParams {
+  moe_block_norm_args a;
+  int wpr, groups;
+};
+
+template <typename X, typename B, int ITEMS>
+__global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(FwdParams p) {
+  // one buffer per reduction and row parity: a row's sums are read behind its
+  // own barrier, and the buffer is written again two barriers later
+  __shared__ float red_b[2][1][kMaxWaves], red_r[2][1][kMaxWaves];
+  int par = 0;
+  const moe_block_norm_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave / p.wpr, first_wave = grp * p.wpr;
+  const int gt = tid - first_wave * 64, stride = p.wpr * 64;
+  const int H = a.H;
+  const float inv_h = 1.0f / (float)H;
+  const bool has_b = a.b != nullptr;
+
+  for (int row0 = blockIdx.x * p.groups; row0 < a.T; row0 += gridDim.x * p.groups, par ^= 1) {
+    const int row = row0 + grp;
+    const bool live = row < a.T;
+    Vec8<X> xv[ITEMS];
+    Vec8<B> bv[ITEMS];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      xv[i].zero();
+      bv[i].zero();
+      if (live && c < H) {
+        xv[i].load(static_cast<const X*>(a.x) + (long long)row * a.ldx + c, H - c);
+        if (has_b) bv[i].load(static_cast<const B*>(a.b) + (long long)row * a.ldb + c, H - c);
+      }
+    }
+    float inv_b = 1.0f;
+    if (has_b && a.w_post) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        float b[8];
+        bv[i].get(b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(b[j], b[j], sum[0]);
+      }
+      row_sums(sum, red_b[par], wave, lane, first_wave, p.wpr);
+      inv_b = 1.0f / __builtin_sqrtf(sum[0] * inv_h + a.eps);
+    }
+    float r[ITEMS][8];
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      xv[i].get(r[i]);
+      if (has_b && live && c < H) {
+        float b[8], s[8];
+        bv[i].get(b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = a.beta * inv_b;
+        if (a.w_post) {
+          Vec8<float> w;
+          float f[8];
+          w.load(a.w_post + c, H - c);
+          w.get(f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] *= f[j];
+        }
+        if (a.gate_mode == MOE_GATE_TOKEN) {
+          const float g = static_cast<const float*>(a.gate)[row];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] *= g;
+        } else if (a.gate_mode == MOE_GATE_CHANNEL) {
+          Vec8<float> w;
+          float f[8];
+          w.load(static_cast<const float*>(a.gate) + c, H - c);
+          w.get(f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] *= f[j];
+        } else if (a.gate_mode == MOE_GATE_FULL) {
+          Vec8<B> w;
+          float f[8];
+          w.load(static_cast<const B*>(a.gate) + (long long)row * a.ldg + c, H - c);
+          w.get(f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[j] *= f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = __builtin_fmaf(b[j], s[j], a.alpha * r[i][j]);
+        Vec8<X>::store(static_cast<X*>(a.r) + (long long)row * a.ldr + c, r[i], H - c);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[0] = __builtin_fmaf(r[i][j], r[i][j], sum[0]);
+    }
+    if (!a.h) continue;
+    // h comes from r before its rounding: one rounding between x, b and h
+    row_sums(sum, red_r[par], wave, lane, first_wave, p.wpr);
+    const float inv_r = 1.0f / __builtin_sqrtf(sum[0] * inv_h + a.eps);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      if (live && c < H) {
+        Vec8<float> w;
+        float f[8];
+        w.load(a.w_pre + c, H - c);
+        w.get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= r[i][j] * inv_r;
+        Vec8<B>::store(static_cast<B*>(a.h) + (long long)row * a.ldh + c, f, H - c);
+      }
+    }
+  }
+}
+
+// ---- backward
+
+// Rows are handed out block by block (a persistent grid), so that each
+// thread keeps the running sums of its channels' dw_pre, dw_post and dgate in
+// registers over all its rows; a second kernel adds the workgroups' partial
+// sums in workgroup order.
+struct BwdParams {
+  moe_block_norm_bwd_args a;
+  int wpr, groups;
+  float* part;      // [3][blocks * groups][H]: dw_pre, dw_post, dgate
+};
+
+template <typename X, typename B, int ITEMS>
+__global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_kernel(BwdParams p) {
+  __shared__ float red_a[2][3][kMaxWaves], red_c[2][1][kMaxWaves];   // by row parity, as above
+  int par = 0;
+  const moe_block_norm_bwd_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave / p.wpr, first_wave = grp * p.wpr;
+  const int gt = tid - first_wave * 64, stride = p.wpr * 64;
+  const int H = a.H;
+  const float inv_h = 1.0f / (float)H;
+  const bool has_b = a.b != nullptr, post = has_b && a.w_post;
+
+  float acc_pre[ITEMS][8] = {}, acc_post[ITEMS][8] = {}, acc_gate[ITEMS][8] = {};
+  float w_pre[ITEMS][8] = {}, w_post[ITEMS][8], gate_c[ITEMS][8];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = (gt + i * stride) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w_post[i][j] = gate_c[i][j] = 1.0f;
+    if (c < H) {
+      Vec8<float> w;
+      if (a.dh) {
+        w.load(a.w_pre + c, H - c);
+        w.get(w_pre[i]);
+      }
+      if (post) {
+        w.load(a.w_post + c, H - c);
+        w.get(w_post[i]);
+      }
+      if (a.gate_mode == MOE_GATE_CHANNEL) {
+        w.load(static_cast<const float*>(a.gate) + c, H - c);
+        w.get(gate_c[i]);
+      }
+    }
+  }
+
+  for (int row0 = blockIdx.x * p.groups; row0 < a.T; row0 += gridDim.x * p.groups, par ^= 1) {
+    const int row = row0 + grp;
+    const bool live = row < a.T;
+    Vec8<X> rv[ITEMS], drv[ITEMS];
+    Vec8<B> bv[ITEMS], dhv[ITEMS], gv[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      rv[i].zero(), drv[i].zero(), bv[i].zero(), dhv[i].zero(), gv[i].zero();
+      if (live && c < H) {
+        if (a.dh) {
+          rv[i].load(static_cast<const X*>(a.r) + (long long)row * a.ldr + c, H - c);
+          dhv[i].load(static_cast<const B*>(a.dh) + (long long)row * a.lddh + c, H - c);
+        }
+        if (a.dr) drv[i].load(static_cast<const X*>(a.dr) + (long long)row * a.lddr + c, H - c);
+        if (has_b) bv[i].load(static_cast<const B*>(a.b) + (long long)row * a.ldb + c, H - c);
+        if (a.gate_mode == MOE_GATE_FULL)
+          gv[i].load(static_cast<const B*>(a.gate) + (long long)row * a.ldg + c, H - c);
+      }
+    }
+    const float gate_t =
+        live && a.gate_mode == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    float s[3] = {0.0f, 0.0f, 0.0f};       // r^2, dh w_pre r, b^2
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      float r[8], dh[8], b[8];
+      rv[i].get(r), dhv[i].get(dh), bv[i].get(b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0] = __builtin_fmaf(r[j], r[j], s[0]);
+        s[1] = __builtin_fmaf(dh[j] * w_pre[i][j], r[j], s[1]);
+        s[2] = __builtin_fmaf(b[j], b[j], s[2]);
+      }
+    }
+    row_sums(s, red_a[par], wave, lane, first_wave, p.wpr);
+    const float inv_r = 1.0f / __builtin_sqrtf(s[0] * inv_h + a.eps);
+    const float inv_b = post ? 1.0f / __builtin_sqrtf(s[2] * inv_h + a.eps) : 1.0f;
+    const float m_r = s[1] * inv_r * inv_h;      // mean(v r^)
+    float d[ITEMS][8], t3[1] = {0.0f};           // t3: sum of u b^ (before a token gate)
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      float r[8], dh[8], b[8];
+      rv[i].get(r), dhv[i].get(dh), bv[i].get(b), drv[i].get(d[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float rh = r[j] * inv_r;
+        acc_pre[i][j] = __builtin_fmaf(dh[j], rh, acc_pre[i][j]);
+        d[i][j] += inv_r * (dh[j] * w_pre[i][j] - rh * m_r);
+      }
+      if (a.dx && live && c < H) {
+        float dx[8];
+        const float al = has_b ? a.alpha : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dx[j] = al * d[i][j];
+        Vec8<X>::store(static_cast<X*>(a.dx) + (long long)row * a.lddx + c, dx, H - c);
+      }
+      if (has_b) {
+        float g[8], dg[8];
+        gv[i].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float bh = b[j] * inv_b, dn0 = a.beta * d[i][j], n = bh * w_post[i][j];
+          const float gj = a.gate_mode == MOE_GATE_FULL ? g[j] : gate_c[i][j];
+          dg[j] = dn0 * n;
+          acc_gate[i][j] += dg[j];
+          t3[0] = __builtin_fmaf(dg[j], gj, t3[0]);
+          acc_post[i][j] = __builtin_fmaf(dn0 * gj * gate_t, bh, acc_post[i][j]);
+          d[i][j] = dn0 * gj * gate_t * w_post[i][j];     // u
+        }
+        if (a.gate_mode == MOE_GATE_FULL && a.dgate && live && c < H)
+          Vec8<B>::store(static_cast<B*>(a.dgate) + (long long)row * a.lddg + c, dg, H - c);
+      }
+    }
+    if (!has_b) continue;
+    if (post || a.gate_mode == MOE_GATE_TOKEN) row_sums(t3, red_c[par], wave, lane, first_wave, p.wpr);
+    if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && live && gt == 0)
+      static_cast<float*>(a.dgate)[row] = t3[0];
+    const float m_b = post ? t3[0] * gate_t * inv_h : 0.0f;     // mean(u b^)
+    if (a.db && live) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int c = (gt + i * stride) * 8;
+        if (c < H) {
+          float b[8];
+          bv[i].get(b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[i][j] = inv_b * (d[i][j] - b[j] * inv_b * m_b);
+          Vec8<B>::store(static_cast<B*>(a.db) + (long long)row * a.lddb + c, d[i], H - c);
+        }
+      }
+    }
+  }
+
+  const long long slot = (long long)blockIdx.x * p.groups + grp;
+  const long long plane = (long long)gridDim.x * p.groups * H;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = (gt + i * stride) * 8;
+    if (c < H) {
+      float* o = p.part + slot * H + c;
+      if (a.dw_pre) Vec8<float>::store(o, acc_pre[i], H - c);
+      if (a.dw_post) Vec8<float>::store(o + plane, acc_post[i], H - c);
+      if (a.dgate && a.gate_mode == MOE_GATE_CHANNEL)
+        Vec8<float>::store(o + 2 * plane, acc_gate[i], H - c);
+    }
+  }
+}
+
+// out[c] = sum over the slots of part[slot][c], 64 channels a workgroup, four
+// slot quarters side by side, added in order (blockIdx.y picks the plane).
+__global__ __launch_bounds__(256) void channel_sum_kernel(const float* part, int slots, int H,
+                                                           float* o0, float* o1, float* o2) {
+  __shared__ float s[4][64];
+  float* out = blockIdx.y == 0 ? o0 : (blockIdx.y == 1 ? o1 : o2);
+  if (!out) return;
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  const float* src = part + (long long)blockIdx.y * slots * H;
+  float t = 0.0f;
+  if (c < H) {
+    const int lo = (int)((long long)slots * q / 4), hi = (int)((long long)slots * (q + 1) / 4);
+    for (int i = lo; i < hi; ++i) t += src[(long long)i * H + c];
+  }
+  s[q][lane] = t;
+  __syncthreads();
+  if (q == 0 && c < H) out[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+}
+
+int bwd_blocks(int T, int H, int cus) {
+  const RowShape s = row_shape(H);
+  const int need = (T + s.groups - 1) / s.groups;
+  return need < cus ? need : cus;
+}
+
+constexpr int kMaxCus = 256;    // workspace bound: blocks never exceed this
+
+template <typename P>
+using kernel_t = void (*)(P);
+
+template <typename P>
+kernel_t<P> pick(kernel_t<P> (&table)[2][2][2], moe_dtype_t x, moe_dtype_t b, int items) {
+  return table[x == MOE_F32][b == MOE_F32][items - 1];
+}
+
+bool bad_ld(const void* p, long long ld, int H) { return p && ld < H; }
+
+}  // namespace
+
+extern "C" moe_status_t moe_block_norm(const moe_block_norm_args* args, hipStream_t stream) {
+  if (!args) return MOE_ERR_NULL;
+  const moe_block_norm_args& a = *args;
+  if (a.T < 0 || a.H < 1 || a.H > kMaxWidth || !(a.eps > 0.0f)) return MOE_ERR_SHAPE;
+  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) || a.gate_mode < MOE_GATE_NONE ||
+      a.gate_mode > MOE_GATE_FULL)
+    return MOE_ERR_UNSUPPORTED;
+  if (bad_ld(a.x, a.ldx, a.H) || bad_ld(a.b, a.ldb, a.H) || bad_ld(a.h, a.ldh, a.H) ||
+      (a.b && bad_ld(a.r, a.ldr, a.H)) ||
+      (a.gate_mode == MOE_GATE_FULL && bad_ld(a.gate, a.ldg, a.H)))
+    return MOE_ERR_SHAPE;
+  if (a.T == 0) return MOE_OK;
+  if (!a.x || (a.b && !a.r) || (!a.b && !a.h) || (a.h && !a.w_pre) ||
+      (a.b && a.gate_mode != MOE_GATE_NONE && !a.gate))
+    return MOE_ERR_NULL;
+  if (!element_aligned(a.x, a.x_dtype) || !element_aligned(a.r, a.x_dtype) ||
+      !element_aligned(a.b, a.b_dtype) || !element_aligned(a.h, a.b_dtype) ||
+      !element_aligned(a.w_pre, MOE_F32) || !element_aligned(a.w_post, MOE_F32) ||
+      !element_aligned(a.gate, a.gate_mode == MOE_GATE_FULL ? a.b_dtype : MOE_F32))
+    return MOE_ERR_ALIGN;
+  if (moe_status_t s = check_device()) return s;
+  const RowShape s = row_shape(a.H);
+  FwdParams p{a, s.wpr, s.groups};
+  if (!a.b) p.a.gate_mode = MOE_GATE_NONE;
+  static kernel_t<FwdParams> table[2][2][2] = {
+      {{block_norm_kernel<bf16_t, bf16_t, 1>, block_norm_kernel<bf16_t, bf16_t, 2>},
+       {block_norm_kernel<bf16_t, float, 1>, block_norm_kernel<bf16_t, float, 2>}},
+      {{block_norm_kernel<float, bf16_t, 1>, block_norm_kernel<float, bf16_t, 2>},
+       {block_norm_kernel<float, float, 1>, block_norm_kernel<float, float, 2>}}};
+  const int blocks = (a.T + s.groups - 1) / s.groups;
+  hipLaunchKernelGGL(pick(table, a.x_dtype, a.b_dtype, s.items), dim3(blocks),
+                     dim3(s.wpr * s.groups * 64), 0, stream, p);
+  return launch_status();
+}
+
+extern "C" size_t moe_block_norm_backward_workspace_bytes(int T, int H) {
+  if (T <= 0 || H <= 0 || H > kMaxWidth) return 0;
+  return (size_t)bwd_blocks(T, H, kMaxCus) * row_shape(H).groups * 3 * H * sizeof(float);
+}
+
+extern "C" moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* args, void* ws,
+                                                size_t ws_bytes, hipStream_t stream) {
+  if (!args) return MOE_ERR_NULL;
+  const moe_block_norm_bwd_args& a = *args;
+  if (a.T < 0 || a.H < 1 || a.H > kMaxWidth || !(a.eps > 0.0f)) return MOE_ERR_SHAPE;
+  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) || a.gate_mode < MOE_GATE_NONE ||
+      a.gate_mode > MOE_GATE_FULL)
+    return MOE_ERR_UNSUPPORTED;
+  const bool full = a.gate_mode == MOE_GATE_FULL;
+  if (bad_ld(a.r, a.ldr, a.H) || bad_ld(a.dr, a.lddr, a.H) || bad_ld(a.dh, a.lddh, a.H) ||
+      bad_ld(a.b, a.ldb, a.H) || bad_ld(a.dx, a.lddx, a.H) || bad_ld(a.db, a.lddb, a.H) ||
+      (full && (bad_ld(a.gate, a.ldg, a.H) || bad_ld(a.dgate, a.lddg, a.H))))
+    return MOE_ERR_SHAPE;
+  const bool sums = a.dw_pre || a.dw_post || (a.dgate && a.gate_mode == MOE_GATE_CHANNEL);
+  if (a.T > 0) {
+    if ((!a.dr && !a.dh) || (a.dh && (!a.r || !a.w_pre)) || (a.dw_pre && !a.dh) ||
+        (!a.b && (a.db || a.dgate || a.dw_post)) || (a.dw_post && !a.w_post) ||
+        (a.b && a.gate_mode != MOE_GATE_NONE && !a.gate) ||
+        (a.dgate && a.gate_mode == MOE_GATE_NONE))
+      return MOE_ERR_NULL;
+    const moe_dtype_t gd = full ? a.b_dtype : MOE_F32;
+    if (!element_aligned(a.r, a.x_dtype) || !element_aligned(a.dr, a.x_dtype) ||
+        !element_aligned(a.dx, a.x_dtype) || !element_aligned(a.dh, a.b_dtype) ||
+        !element_aligned(a.b, a.b_dtype) || !element_aligned(a.db, a.b_dtype) ||
+        !element_aligned(a.w_pre, MOE_F32) || !element_aligned(a.w_post, MOE_F32) ||
+        !element_aligned(a.gate, gd) || !element_aligned(a.dgate, gd) ||
+        !element_aligned(a.dw_pre, MOE_F32) || !element_aligned(a.dw_post, MOE_F32))
+      return MOE_ERR_ALIGN;
+    if (sums) {
+      if (!ws || ws_bytes < moe_block_norm_backward_workspace_bytes(a.T, a.H))
+        return MOE_ERR_WORKSPACE;
+      if (!aligned16(ws)) return MOE_ERR_ALIGN;
+    }
+  } else if (!sums) {
+    return MOE_OK;
+  }
+  if (moe_status_t s = check_device()) return s;
+  const RowShape s = row_shape(a.H);
+  int slots = 0;
+  if (a.T > 0) {
+    int cus = cu_count();
+    if (cus < 1 || cus > kMaxCus) cus = kMaxCus;
+    const int blocks = bwd_blocks(a.T, a.H, cus);
+    slots = blocks * s.groups;
+    BwdParams p{a, s.wpr, s.groups, static_cast<float*>(ws)};
+    if (!a.b) p.a.gate_mode = MOE_GATE_NONE;
+    static kernel_t<BwdParams> table[2][2][2] = {
+        {{block_norm_bwd_kernel<bf16_t, bf16_t, 1>, block_norm_bwd_kernel<bf16_t, bf16_t, 2>},
+         {block_norm_bwd_kernel<bf16_t, float, 1>, block_norm_bwd_kernel<bf16_t, float, 2>}},
+        {{block_norm_bwd_kernel<float, bf16_t, 1>, block_norm_bwd_kernel<float, bf16_t, 2>},
+         {block_norm_bwd_kernel<float, float, 1>, block_norm_bwd_kernel<float, float, 2>}}};
+    hipLaunchKernelGGL(pick(table, a.x_dtype, a.b_dtype, s.items), dim3(blocks),
+                       dim3(s.wpr * s.groups * 64), 0, stream, p);
+    if (moe_status_t st = launch_status()) return st;
+  }
+  if (sums)
+    hipLaunchKernelGGL(channel_sum_kernel, dim3((a.H + 63) / 64, 3), dim3(256), 0, stream,
+                       static_cast<const float*>(ws), slots, a.H, a.dw_pre, a.dw_post,
+                       a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr);
+  return launch_status();
+}

@@ -1,0 +1,151 @@
+// The experts' gated activation in bf16 or float, and its backward pass.
+//
+//   h = silu(g) u,  silu(g) = g s,  s = 1 / (1 + exp(-g)),  a = [g | u]
+// Backward of w h with respect to g, u and w (w the row's combine gate, dh the
+// gradient of the expert row before the gate):
+//   dg = w dh u (s + silu(g) (1 - s)),  du = w dh silu(g),  dw = sum_c h dh
+// and w h, the rows that the weight gradient of the second product reads.
+#include "rows.h"
+
+namespace {
+
+using namespace moe;
+
+// s and silu(g).  exp(-g) overflows to infinity below g = -88.7, where s and
+// silu(g) are 0 to float precision, as they should be.
+__device__ __forceinline__ void sigmoid_silu(float g, float& s, float& silu) {
+  s = 1.0f / (1.0f + expf(-g));
+  silu = g * s;
+}
+
+// One thread per vector of 8 columns, rows one behind the other.
+template <typename E>
+__global__ __launch_bounds__(256) void swiglu_kernel(const E* a, long long lda, uint32_t items,
+                                                      int vecs, int I, E* h, long long ldh) {
+  const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+  if (item >= items) return;
+  const uint32_t row = item / (uint32_t)vecs;
+  const int c = (int)(item - row * (uint32_t)vecs) * 8;
+  Vec8<E> gv, uv;
+  gv.load(a + row * lda + c, I - c);
+  uv.load(a + row * lda + I + c, I - c);
+  float g[8], u[8];
+  gv.get(g), uv.get(u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float s, silu;
+    sigmoid_silu(g[j], s, silu);
+    g[j] = silu * u[j];
+  }
+  Vec8<E>::store(h + row * ldh + c, g, I - c);
+}
+
+struct BwdParams {
+  const void *a, *dh;
+  const float* row_gate;
+  void *da, *hg;
+  float* dgate;
+  long long lda, lddh, ldda, ldhg;
+  int R, I, wpr;       // wpr: waves that share a row (1, 2 or 4 of a workgroup's 4)
+};
+
+template <typename E>
+__global__ __launch_bounds__(256) void swiglu_bwd_kernel(BwdParams p) {
+  __shared__ float red[4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave / p.wpr, first = grp * p.wpr;
+  const long long row = (long long)blockIdx.x * (4 / p.wpr) + grp;
+  const bool live = row < p.R;
+  float sum = 0.0f;
+  if (live) {
+    const E* a = static_cast<const E*>(p.a) + row * p.lda;
+    const E* dh = static_cast<const E*>(p.dh) + row * p.lddh;
+    const float w = p.row_gate ? p.row_gate[row] : 1.0f;
+    for (int c = (tid - first * 64) * 8; c < p.I; c += p.wpr * 512) {
+      Vec8<E> gv, uv, dv;
+      gv.load(a + c, p.I - c);
+      uv.load(a + p.I + c, p.I - c);
+      dv.load(dh + c, p.I - c);
+      float g[8], u[8], d[8], hg[8];
+      gv.get(g), uv.get(u), dv.get(d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float s, silu;
+        sigmoid_silu(g[j], s, silu);
+        const float h = silu * u[j], wd = w * d[j];
+        sum = __builtin_fmaf(h, d[j], sum);
+        hg[j] = w * h;
+        g[j] = wd * u[j] * __builtin_fmaf(silu, 1.0f - s, s);
+        u[j] = wd * silu;
+      }
+      E* da = static_cast<E*>(p.da) + row * p.ldda;
+      Vec8<E>::store(da + c, g, p.I - c);
+      Vec8<E>::store(da + p.I + c, u, p.I - c);
+      if (p.hg) Vec8<E>::store(static_cast<E*>(p.hg) + row * p.ldhg + c, hg, p.I - c);
+    }
+  }
+  if (!p.dgate) return;
+  sum = wave_sum(sum);
+  if (p.wpr > 1) {
+    if (lane == 0) red[wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int i = 0; i < p.wpr; ++i) sum += red[first + i];
+  }
+  if (live && tid == first * 64) p.dgate[row] = sum;
+}
+
+}  // namespace
+
+extern "C" moe_status_t moe_swiglu(const void* a, moe_dtype_t dt, int R, int I, long long lda,
+                                   void* h, long long ldh, hipStream_t stream) {
+  if (R < 0 || I < 0 || I > (1 << 24) || lda < 2LL * I || ldh < I) return MOE_ERR_SHAPE;
+  if (!valid_dtype(dt)) return MOE_ERR_UNSUPPORTED;
+  if (R == 0 || I == 0) return MOE_OK;
+  if (!a || !h) return MOE_ERR_NULL;
+  if (!element_aligned(a, dt) || !element_aligned(h, dt)) return MOE_ERR_ALIGN;
+  if (moe_status_t s = check_device()) return s;
+  const int vecs = (I + 7) / 8;
+  const int slab = (1 << 30) / vecs;      // rows whose vectors count below 2^30
+  for (long long r0 = 0; r0 < R; r0 += slab) {
+    const uint32_t items = (uint32_t)(R - r0 < slab ? R - r0 : slab) * (uint32_t)vecs;
+    if (dt == MOE_BF16)
+      hipLaunchKernelGGL(swiglu_kernel<bf16_t>, dim3((items + 255) / 256), dim3(256), 0, stream,
+                         static_cast<const bf16_t*>(a) + r0 * lda, lda, items, vecs, I,
+                         static_cast<bf16_t*>(h) + r0 * ldh, ldh);
+    else
+      hipLaunchKernelGGL(swiglu_kernel<float>, dim3((items + 255) / 256), dim3(256), 0, stream,
+                         static_cast<const float*>(a) + r0 * lda, lda, items, vecs, I,
+                         static_cast<float*>(h) + r0 * ldh, ldh);
+    if (moe_status_t s = launch_status()) return s;
+  }
+  return MOE_OK;
+}
+
+extern "C" moe_status_t moe_swiglu_backward(const void* a, const void* dh, moe_dtype_t dt, int R,
+                                            int I, long long lda, long long lddh,
+                                            const float* row_gate, void* da, long long ldda,
+                                            float* dgate, void* hg, long long ldhg,
+                                            hipStream_t stream) {
+  if (R < 0 || I < 0 || I > (1 << 24) || lda < 2LL * I || lddh < I || ldda < 2LL * I ||
+      (hg && ldhg < I))
+    return MOE_ERR_SHAPE;
+  if (!valid_dtype(dt)) return MOE_ERR_UNSUPPORTED;
+  if (R == 0) return MOE_OK;
+  if (I > 0 && (!a || !dh || !da)) return MOE_ERR_NULL;
+  if (!element_aligned(a, dt) || !element_aligned(dh, dt) || !element_aligned(da, dt) ||
+      !element_aligned(hg, dt) || !element_aligned(row_gate, MOE_F32) ||
+      !element_aligned(dgate, MOE_F32))
+    return MOE_ERR_ALIGN;
+  if (moe_status_t s = check_device()) return s;
+  const BwdParams p{a, dh, row_gate, da, hg, dgate, lda, lddh, ldda, ldhg, R, I,
+                    R >= 8192 ? 1 : (R >= 4096 ? 2 : 4)};
+  const int rows = 4 / p.wpr;
+  const dim3 grid((unsigned)((R + (long long)rows - 1) / rows));
+  if (dt == MOE_BF16)
+    hipLaunchKernelGGL(swiglu_bwd_kernel<bf16_t>, grid, dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, grid, dim3(256), 0, stream, p);
+  return launch_status();
+}

@@ -463,6 +463,218 @@ size_t moe_layer_workspace_bytes(int T, int H, int N, int k, int I, int with_sha
 moe_status_t moe_layer_forward(const moe_layer_args* args, void* ws, size_t ws_bytes,
                                hipStream_t stream);
 
+/*
+ * ---- The layer's training in bf16 and the block around it.
+ *
+ * The entry points below take bf16 or float tensors (moe_dtype_t) and return
+ * results of the same kinds; all sums, statistics and products are formed in
+ * float (the gradient norm in double) and each output is rounded once.
+ * Non-finite inputs are allowed: they reach the outputs that depend on them
+ * and no others.  Unless stated otherwise, outputs must not overlap inputs.
+ */
+
+/* How a block's gate is shared: not there, one value per channel (float [H]),
+ * per token (float [T]), or one per element (b's type, [T,H]). */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,
+  MOE_GATE_TOKEN = 2,
+  MOE_GATE_FULL = 3
+} moe_gate_t;
+
+/*
+ * The norms around a block, fused with its gate and the residual scale: the
+ * block's output is normalised, gated, scaled and added to the residual
+ * stream, and the stream is normalised for the next block.  Per token t:
+ *   n = b / sqrt(mean_h(b^2) + eps) * w_post       (n = b when w_post is NULL)
+ *   r = alpha * x + beta * gate * n
+ *   h = r / sqrt(mean_h(r^2) + eps) * w_pre        (not formed when h is NULL)
+ * Without a block output (b NULL: the first norm of a model) r = x, which is
+ * not written again, and only h is.  h is formed from r before its rounding.
+ * x, r [T,H] of x_dtype; b, h and a MOE_GATE_FULL gate [T,H] of b_dtype; w_pre,
+ * w_post float [H].  Row strides (ld*, in elements) are at least H and free
+ * otherwise; pointers need the alignment of their element type only.  r may
+ * be x and h may be b (the same pointer and stride).
+ * Requires 1 <= H <= 16384, eps > 0 (MOE_ERR_SHAPE).
+ */
+typedef struct {
+  int T, H;
+  moe_dtype_t x_dtype, b_dtype;
+  const void* x; long long ldx;
+  const void* b; long long ldb;
+  const float* w_pre;
+  const float* w_post;
+  int gate_mode;
+  const void* gate; long long ldg;
+  float alpha, beta, eps;
+  void* r; long long ldr;
+  void* h; long long ldh;
+} moe_block_norm_args;
+
+moe_status_t moe_block_norm(const moe_block_norm_args* args, hipStream_t stream);
+
+/*
+ * Its backward pass, from the stream r that the forward pass wrote (x when
+ * there was no block output) and b.  dr is the gradient that reaches r from
+ * its other use (the next residual sum; NULL: none), dh the gradient of h
+ * (NULL when h was not formed); one of them must be there.
+ *   d = dr + d(h)/d(r) dh,  dx = alpha * d (d itself without b),
+ *   db = d(n)/d(b) (beta * gate * d),  and the sums over tokens
+ *   dw_pre [H] (dh r / rms(r)), dw_post [H] (beta gate d b / rms(b)), and
+ *   dgate = beta * d * n, summed over tokens (MOE_GATE_CHANNEL, float [H]) or
+ *   channels (MOE_GATE_TOKEN, float [T]), or as it is (MOE_GATE_FULL, b_dtype).
+ * Each of dx, db, dw_pre, dw_post, dgate may be NULL: it is not wanted.  dx may
+ * be dr and db may be b or dh.  The sums over tokens go through ws (device,
+ * 16-byte aligned, moe_block_norm_backward_workspace_bytes(T, H) bytes; may be
+ * NULL when none of them is wanted) and do not depend on how the launch is
+ * scheduled.  With T = 0 the sums that are wanted are written as zeros.
+ */
+typedef struct {
+  int T, H;
+  moe_dtype_t x_dtype, b_dtype;
+  const void* r; long long ldr;
+  const void* dr; long long lddr;
+  const void* dh; long long lddh;
+  const void* b; long long ldb;
+  const float* w_pre;
+  const float* w_post;
+  int gate_mode;
+  const void* gate; long long ldg;
+  float alpha, beta, eps;
+  void* dx; long long lddx;
+  void* db; long long lddb;
+  float* dw_pre;
+  float* dw_post;
+  void* dgate; long long lddg;
+} moe_block_norm_bwd_args;
+
+size_t moe_block_norm_backward_workspace_bytes(int T, int H);
+moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* args, void* ws,
+                                     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Grouped bf16 product over ragged row groups, for every row r of group g
+ * (group_offsets[g] <= r < group_offsets[g+1]):
+ *   out[r, c] = row_scale[r] * sum_k A[src(r), k] * B[g](c, k)
+ * with src(r) = a_row_index[r] (fused gather) or r, and row_scale NULL meaning 1.
+ * b_layout MOE_B_NK: b [G, n_out, k_dim] (the forward product, weights [out,
+ * in]); MOE_B_KN: b [G, k_dim, n_out] (the input gradient, from the same
+ * weights).  a bf16 [a_rows, lda], out bf16 or float [total_rows, ldo].
+ * group_offsets int32 [G+1] on the device, non-decreasing, first 0 and last
+ * total_rows (values outside [0, total_rows] are clamped); groups may be empty;
+ * gathered indices are clamped to a_rows.  Products are summed in float in an
+ * order that depends on the sizes alone.
+ * Requires k_dim, n_out, lda, ldo multiples of 8, lda >= k_dim, ldo >= n_out, and
+ * a_rows >= total_rows without a_row_index (MOE_ERR_SHAPE); a, b, out 16-byte
+ * aligned; 1 <= G <= 1025, n_out * k_dim < 2^30, and with a_row_index
+ * a_rows * lda < 2^30 (MOE_ERR_UNSUPPORTED).
+ */
+typedef enum { MOE_B_NK = 0, MOE_B_KN = 1 } moe_b_layout_t;
+
+typedef struct {
+  const void* a; long long lda; int a_rows;
+  const int32_t* a_row_index;
+  const void* b;
+  int b_layout;
+  const int32_t* group_offsets;
+  int num_groups, total_rows, n_out, k_dim;
+  moe_dtype_t out_dtype;
+  void* out; long long ldo;
+  const float* row_scale;
+} moe_gemm_bf16_args;
+
+moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hipStream_t stream);
+
+/*
+ * Weight gradients of the same groups:
+ *   out[g][i, j] = sum over rows r of group g of A[srcA(r), i] * B[srcB(r), j]
+ * (+ the former out[g][i, j] with accumulate).  a bf16 [a_rows, lda] (n columns:
+ * the output channels' gradient), b bf16 [b_rows, ldb] (k columns: the product's
+ * input), each optionally gathered through its row index; out bf16 or float
+ * [G, n, k], dense.  A group without rows gives zeros (or keeps its former
+ * value with accumulate).  ws: device scratch of
+ * moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k) bytes, 16-byte
+ * aligned (may be NULL when that is 0).  Deterministic.
+ * Requires n, k, lda, ldb multiples of 8 and the row bounds of
+ * moe_grouped_gemm_bf16 for both operands.
+ */
+typedef struct {
+  const void* a; long long lda; int a_rows;
+  const int32_t* a_row_index;
+  const void* b; long long ldb; int b_rows;
+  const int32_t* b_row_index;
+  const int32_t* group_offsets;
+  int num_groups, total_rows, n, k;
+  moe_dtype_t out_dtype;
+  void* out;
+  int accumulate;
+} moe_wgrad_bf16_args;
+
+size_t moe_grouped_wgrad_bf16_workspace_bytes(int num_groups, int total_rows, int n, int k);
+moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, void* ws, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/*
+ * The experts' gated activation on unquantised rows, a = [g | u] (gate columns,
+ * then up columns; the order of W1's rows):
+ *   h[r, c] = silu(a[r, c]) * a[r, I + c],  silu(g) = g / (1 + exp(-g))
+ * a [R, 2I] (row stride lda), h [R, I] (row stride ldh), both of dtype dt.
+ *
+ * moe_swiglu_backward: the gradient of row_gate[r] * h[r, :], the row weighted
+ * by its combine gate (row_gate float [R]; NULL: all 1), given dh [R, I], the
+ * gradient of the expert row before its gate (the input gradient of the second
+ * product, from the layer's output gradient gathered by token):
+ *   da[r, c]     = row_gate[r] dh u silu'(g),  da[r, I + c] = row_gate[r] dh silu(g)
+ *   dgate[r]     = sum_c h dh                    float [R], or NULL
+ *   hg[r, c]     = row_gate[r] h                 (dt), or NULL: with the gathered
+ *                  output gradient, the operands of the second weight gradient
+ * da may be a (same stride).  Any I up to 2^24, any strides and element alignment.
+ */
+moe_status_t moe_swiglu(const void* a, moe_dtype_t dt, int R, int I, long long lda, void* h,
+                        long long ldh, hipStream_t stream);
+moe_status_t moe_swiglu_backward(const void* a, const void* dh, moe_dtype_t dt, int R, int I,
+                                 long long lda, long long lddh, const float* row_gate, void* da,
+                                 long long ldda, float* dgate, void* hg, long long ldhg,
+                                 hipStream_t stream);
+
+/*
+ * Global gradient norm over many tensors, and clipping by it:
+ *   norm = sqrt(sum over tensors and elements of src^2)       (summed in double)
+ *   coef = min(1, max_norm / (norm + 1e-6)); 1 when the norm is not finite, so
+ *          that gradients with an infinity or NaN are left for the caller to see
+ *   dst  = coef * src, rounded once to dst's type
+ * moe_grad_table packs a list of dense tensors (HOST array; src and dst device
+ * pointers, dst == src for clipping in place) into `table` (HOST memory of
+ * moe_grad_table_bytes(n) bytes), which the caller copies to the device once and
+ * keeps while the tensors stay where they are; *total_chunks goes into the
+ * calls below.  Tensors may be empty and need the alignment of their element
+ * type only.  A dst that overlaps any other tensor of the list, or its own src
+ * in part, is MOE_ERR_UNSUPPORTED.
+ * moe_grad_norm: *sumsq (double) and *norm (float), device, each NULL to skip.
+ * moe_grad_scale: the scaling alone, from a given sum of squares (for gradients
+ * that are spread over several GPUs: sum the ranks' sumsq in between).
+ * moe_grad_clip: both, without a host wait.  result, when not NULL, receives
+ * float {norm, coef}.  max_norm >= 0.  ws: device scratch, 8-byte aligned, of
+ * moe_grad_norm_workspace_bytes(total_chunks) bytes.
+ */
+typedef struct {
+  const void* src;
+  void* dst;
+  long long numel;
+  moe_dtype_t src_dtype, dst_dtype;
+} moe_grad_tensor;
+
+size_t moe_grad_table_bytes(int n);
+moe_status_t moe_grad_table(const moe_grad_tensor* tensors, int n, void* table, size_t table_bytes,
+                            long long* total_chunks);
+size_t moe_grad_norm_workspace_bytes(long long total_chunks);
+moe_status_t moe_grad_norm(const void* table, int n, long long total_chunks, void* ws,
+                           size_t ws_bytes, double* sumsq, float* norm, hipStream_t stream);
+moe_status_t moe_grad_scale(const void* table, int n, long long total_chunks, const double* sumsq,
+                            float max_norm, float* result, hipStream_t stream);
+moe_status_t moe_grad_clip(const void* table, int n, long long total_chunks, void* ws,
+                           size_t ws_bytes, float max_norm, float* result, hipStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* moe_status_str(moe_status_t status);
 /* hipError_t of the most recent MOE_ERR_HIP on this thread (0 if none). */

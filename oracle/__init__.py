@@ -32,6 +32,8 @@ Modules:
   balance  sequence-wise balance statistic (f_i P_i per sequence).
   layer    the whole layer chained from the pieces above.
   backward FP8 input-gradient and weight-gradient GEMMs (token-tile quantiser).
+  train    the bf16 training operators (block norms, grouped products, gated
+           activation, gradient clipping) with their backward passes.
 
 Parity status: every function above is pinned by ``tests/test_oracle_*.py``
 against closed forms, brute force, invariants or library special cases; none
