@@ -1,7 +1,39 @@
 // Grouped bf16 products of the experts over ragged row groups:
 //   forward and input gradient   C[r, c] = s[r] sum_k A[src(r), k] B[g](c, k)
-//   weight gradient              dW[g][n, k] = sum_{r in g} A[srcA(r), n] B[srcB(r), k]
+//   weight gradient              dW[g][i, j] = sum_{r in g} A[srcA(r), i] B[srcB(r), j]
 // bf16 operands, float sums (v_mfma_f32_16x16x32_bf16), bf16 or float results.
+//
+// One K loop serves all three (tile_product below).  An operand is either
+// "straight" (the contraction index runs along its rows in memory: both
+// operands of the forward product, the A of the input gradient) or "crossed"
+// (it runs across rows: the weights of the input gradient, both operands of
+// the weight gradient); they differ in how a tile is laid into LDS and read
+// back into MFMA fragments, not in the schedule.
+//
+//   * A workgroup of 8 waves computes a 256 x 256 tile in steps of 64 along
+//     the contraction.  Wave (wm, wn) owns 16-row subtiles 2 i + wm of each
+//     128-row half of A and columns 32 wn .. + 31 of each 128-column half of
+//     B: four quadrants (half of A x half of B) of 16 MFMAs a step, 128 float
+//     accumulators.
+//   * LDS holds two steps of both operands as eight 16 KB half tiles, filled
+//     by direct-to-LDS buffer loads.  Each quadrant is one phase; a phase
+//     reads the fragments that its successor needs and requests one half
+//     tile into the slot that was last read two phases ago, four to five
+//     phases (1 us) before its first use.
+//   * Waves 0-3 and 4-7 (one of each per SIMD) run half a phase apart: while
+//     one group issues its MFMAs the other reads LDS and requests copies.
+//   * Straight half tile: [128 rows][64 k], 16-byte chunks XOR-swizzled by row
+//     so that ds_read_b128 has no bank conflicts.  Crossed half tile: [64 k]
+//     [128 columns], swizzled for ds_read_b64_tr_b16, which hands each lane
+//     four k values of its column.
+//   * Row tiles of a group are of equal height (a multiple of 16 rows), and a
+//     tile of fewer than 256 rows skips the MFMAs of its empty subtiles (the
+//     loop is compiled for each count).
+//   * Rows past a group's end, columns past the matrix and the tail of k are
+//     given offsets beyond the buffer resource's size and read as zero, so
+//     they never meet the group's data, whatever they hold.
+#include <type_traits>
+
 #include "common.h"
 
 namespace {
@@ -9,208 +41,507 @@ namespace {
 using namespace moe;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
 
 constexpr int kMaxGroups = 1025;
-constexpr int kThreads = 256;
-constexpr int BM = 128, BN = 128, BK = 32, kPad = 8;
+constexpr int kThreads = 512;
+constexpr int kTile = 256;                 // rows and columns of a tile
+constexpr int kStep = 64;                  // contraction depth of a step
+constexpr int kHalf = 128 * kStep * 2;     // bytes of a half tile
+constexpr int kLds = 8 * kHalf;            // [A, B][half][step parity]
+constexpr uint32_t kOut = 0x80000000u;     // an offset past every buffer (all are below 2^31)
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
 
-// The group and the row tile inside it of row tile `want` of the list of all
-// groups' row tiles, found by every thread from the device-side offsets.
-__device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int G, int total, int tile,
-                                              int want, int* s_scan, int& g, int& m, int& row0,
-                                              int& rows) {
-  int base = 0;
-  for (int g0 = 0; g0 < G; g0 += kThreads) {
-    const int gi = g0 + threadIdx.x;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// One operand of a tile, as a lane sees it.
+struct Operand {
+  const uint8_t* base;     // straight: the tile's first element; crossed: the step's first row
+  uint32_t bytes;          // straight, gathered: size of the resource
+  uint32_t off[2][2];      // [half][j]: this lane's offsets of its two loads of a half tile
+  uint32_t tail;           // straight: added to the offsets in the last step
+  // crossed
+  const int32_t* index;    // gather, from the group's first row
+  int rows, max_row;       // contraction length; last row of a gathered operand
+  uint32_t ld2;            // row stride in bytes
+};
+
+// Transposing LDS read: the 16 lanes of a group read four rows of 16 values
+// (lane i the values 4 (i & 3) .. + 3 of row i >> 2), and lane c receives column
+// c.  Through a restrict parameter the compiler sees that no copy in flight
+// aliases it; without that it would wait for all of them before every read.
+// The waits that these reads need are the explicit ones of the K loop.
+__device__ __forceinline__ s16x4 read_tr(lds_s16x4_t __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The K loop.  A_X / B_X: crossed operand; A_G / B_G: gathered crossed operand;
+// L0, L1: 16-row subtiles per wave with rows in A's first and second half.
+template <bool A_X, bool B_X, bool A_G, bool B_G, int L0, int L1>
+struct Product {
+  static constexpr int kIdx = 2 * (A_G ? 1 : 0) + 2 * (B_G ? 1 : 0);   // index loads a step
+  f32x4 acc[2][4][2][2];        // [A half][subtile][B half][subtile]
+  bf16x8 a0[4][2], a1[4][2], b0[2][2], b1[2][2];
+  int ia[2][2], ib[2][2];       // gathered rows of the two steps ahead, [step parity][j]
+
+  uint8_t* smem;
+  int wave, lane, n_steps;
+  const Operand &A, &B;
+
+  __device__ __forceinline__ Product(uint8_t* s, int w, int l, int n, const Operand& a, const Operand& b)
+      : smem(s), wave(w), lane(l), n_steps(n), A(a), B(b) {}
+
+  template <bool X, bool G>
+  __device__ __forceinline__ void copy(const Operand& o, uint8_t* slot, int h, int step, const int (&idx)[2]) {
+    step = min(step, n_steps - 1);       // steps past the end repeat the last one, unread
+    uint8_t* dst = slot + wave * 1024;
+    if constexpr (!X) {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(o.base, o.bytes);
+      const uint32_t t = step == n_steps - 1 ? o.tail : 0u;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(dst + j * 8192), 16,
+                                                 (int)(o.off[h][j] | t), step * (kStep * 2), 0, 0);
+    } else if constexpr (!G) {
+      const int left = min(o.rows - step * kStep, kStep);
+      const __amdgpu_buffer_rsrc_t r =
+          make_rsrc(o.base + (long long)step * kStep * o.ld2, (uint32_t)left * o.ld2);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(dst + j * 8192), 16,
+                                                 (int)o.off[h][j], 0, 0, 0);
+    } else {
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(o.base, o.bytes);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool live = step * kStep + 4 * wave + (lane >> 4) + 32 * j < o.rows;
+        int row = idx[j];
+        asm volatile("" : "+v"(row));      // keeps the arithmetic here, phases after the load
+        const uint32_t at = live ? (uint32_t)clampi(row, 0, o.max_row) * o.ld2 : kOut;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(dst + j * 8192), 16,
+                                                 (int)(at + o.off[h][j]), 0, 0, 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_index(const Operand& o, int step, int (&idx)[2]) {
+    const int first = step * kStep + 4 * wave + (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) idx[j] = o.index[min(first + 32 * j, o.rows - 1)];
+  }
+
+  __device__ __forceinline__ uint8_t* slot(int op, int h, int par) {
+    return smem + ((op * 2 + h) * 2 + par) * kHalf;
+  }
+  // MFMA fragment of 16 rows (columns) and 32 k values
+  __device__ __forceinline__ bf16x8 crossed(const uint8_t* s, int blk, int kk) {
+    const int lk = lane >> 4, a = (lane & 15) >> 2, q = lane & 3;
+    const int x = a | ((lk & 1) << 2);
+    const uint8_t* p = s + (kk * 32 + lk * 8 + a) * 256 + (blk ^ x) * 32 + (q >> 1) * 16 + (q & 1) * 8;
+    const s16x4 lo = read_tr((lds_s16x4_t)p);
+    const s16x4 hi = read_tr((lds_s16x4_t)(p + 1024));
+    const bf16x4 l4 = __builtin_bit_cast(bf16x4, lo), h4 = __builtin_bit_cast(bf16x4, hi);
+    return __builtin_shufflevector(l4, h4, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  __device__ __forceinline__ bf16x8 read_a(const uint8_t* s, int i, int kk) {
+    const int blk = 2 * i + (wave & 1);
+    if constexpr (A_X) {
+      return crossed(s, blk, kk);
+    } else {
+      const int r = lane & 15, lk = lane >> 4;
+      return *reinterpret_cast<const bf16x8*>(s + (blk * 16 + r) * 128 + (((lk + 4 * kk) ^ (r >> 1)) << 4));
+    }
+  }
+  __device__ __forceinline__ bf16x8 read_b(const uint8_t* s, int t, int kk) {
+    const int wn = wave >> 1;
+    if constexpr (B_X) {
+      return crossed(s, 2 * wn + t, kk);
+    } else {
+      // fragment row i holds column 8 (i >> 2) + 4 t + (i & 3): the two
+      // subtiles give a lane eight consecutive columns
+      const int a = (lane & 15) >> 2, b = lane & 3, lk = lane >> 4;
+      return *reinterpret_cast<const bf16x8*>(s + (wn * 32 + a * 8 + t * 4 + b) * 128 +
+                                              (((lk + 4 * kk) ^ ((b >> 1) | (a << 1))) << 4));
+    }
+  }
+
+  template <int H, int L>
+  __device__ __forceinline__ void quadrant(const bf16x8 (&a)[4][2], const bf16x8 (&b)[2][2], int hb) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[H][i][hb][t] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][kk], a[i][kk], acc[H][i][hb][t], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  }
+
+  // One step in four phases.  PAR: parity of the step's slots.
+  template <int PAR>
+  __device__ __forceinline__ void step(int s) {
+    // phase 0: rest of A0 and all of B0; quadrant (A0, B0)
+    if constexpr (L0 > 3) {
+      a0[3][0] = read_a(slot(0, 0, PAR), 3, 0);
+      a0[3][1] = read_a(slot(0, 0, PAR), 3, 1);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) b0[t][kk] = read_b(slot(1, 0, PAR), t, kk);
+    copy<A_X, A_G>(A, slot(0, 1, PAR ^ 1), 1, s + 1, ia[PAR ^ 1]);
+    wait_vm<6 + kIdx>();
+    barrier();
+    quadrant<0, L0>(a0, b0, 0);
+    barrier();
+    // phase 1: B1, first of A1; quadrant (A0, B1)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) b1[t][kk] = read_b(slot(1, 1, PAR), t, kk);
+    if constexpr (L1 > 0) {
+      a1[0][0] = read_a(slot(0, 1, PAR), 0, 0);
+      a1[0][1] = read_a(slot(0, 1, PAR), 0, 1);
+    }
+    copy<B_X, B_G>(B, slot(1, 1, PAR ^ 1), 1, s + 1, ib[PAR ^ 1]);
+    barrier();
+    quadrant<0, L0>(a0, b1, 1);
+    barrier();
+    // phase 2: rest of A1; quadrant (A1, B1)
+#pragma unroll
+    for (int i = 1; i < L1; ++i) {
+      a1[i][0] = read_a(slot(0, 1, PAR), i, 0);
+      a1[i][1] = read_a(slot(0, 1, PAR), i, 1);
+    }
+    copy<A_X, A_G>(A, slot(0, 0, PAR), 0, s + 2, ia[PAR]);
+    wait_vm<8 + kIdx>();
+    barrier();
+    quadrant<1, L1>(a1, b1, 1);
+    barrier();
+    // phase 3: most of the next step's A0; quadrant (A1, B0)
+#pragma unroll
+    for (int i = 0; i < (L0 < 3 ? L0 : 3); ++i) {
+      a0[i][0] = read_a(slot(0, 0, PAR ^ 1), i, 0);
+      a0[i][1] = read_a(slot(0, 0, PAR ^ 1), i, 1);
+    }
+    if constexpr (A_G) load_index(A, s + 3, ia[PAR ^ 1]);
+    if constexpr (B_G) load_index(B, s + 3, ib[PAR ^ 1]);
+    __builtin_amdgcn_sched_barrier(0);
+    copy<B_X, B_G>(B, slot(1, 0, PAR), 0, s + 2, ib[PAR]);
+    wait_vm<8 + kIdx>();
+    barrier();
+    quadrant<1, L1>(a1, b0, 0);
+    barrier();
+  }
+
+  __device__ __forceinline__ void run() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) acc[h][i][u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (n_steps == 0) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if constexpr (A_G) load_index(A, s, ia[s]);
+      if constexpr (B_G) load_index(B, s, ib[s]);
+    }
+    copy<A_X, A_G>(A, slot(0, 0, 0), 0, 0, ia[0]);
+    copy<B_X, B_G>(B, slot(1, 0, 0), 0, 0, ib[0]);
+    copy<A_X, A_G>(A, slot(0, 1, 0), 1, 0, ia[0]);
+    copy<B_X, B_G>(B, slot(1, 1, 0), 1, 0, ib[0]);
+    if constexpr (A_G) load_index(A, 2, ia[0]);
+    if constexpr (B_G) load_index(B, 2, ib[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    copy<A_X, A_G>(A, slot(0, 0, 1), 0, 1, ia[1]);
+    copy<B_X, B_G>(B, slot(1, 0, 1), 0, 1, ib[1]);
+    wait_vm<8>();            // A0 and B0 of step 0
+    barrier();
+#pragma unroll
+    for (int i = 0; i < (L0 < 3 ? L0 : 3); ++i) {
+      a0[i][0] = read_a(slot(0, 0, 0), i, 0);
+      a0[i][1] = read_a(slot(0, 0, 0), i, 1);
+    }
+    if (wave >= 4) barrier();     // half a phase behind
+    int s = 0;
+    for (; s + 2 <= n_steps; s += 2) {
+      step<0>(s);
+      step<1>(s + 1);
+    }
+    if (s < n_steps) step<0>(s);
+    if (wave < 4) barrier();
+    wait_vm<0>();            // copies in flight would land in the next user's LDS
+  }
+};
+
+// This lane's offsets of a straight operand (rows[h][j]: the row, relative to
+// the operand's base, of load j of half h; negative: nothing there).
+__device__ __forceinline__ void straight_offsets(Operand& o, const long long (&rows)[2][2], long long ld,
+                                                 int chunk, int K) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      o.off[h][j] = rows[h][j] < 0 ? kOut : (uint32_t)(rows[h][j] * ld * 2) + chunk * 16;
+  const int last = (K - 1) / kStep * kStep;
+  o.tail = last + chunk * 8 < K ? 0u : kOut;
+}
+// and of a crossed operand of `cols` columns from the tile's first one
+__device__ __forceinline__ void crossed_offsets(Operand& o, int wave, int lane, uint32_t ld2, int cols,
+                                                bool gathered) {
+  const int k = 4 * wave + (lane >> 4);
+  const int chunk = (lane & 15) ^ (2 * ((lane >> 4) | (((wave >> 1) & 1) << 2)));
+  o.ld2 = ld2;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      o.off[h][j] = h * 128 + chunk * 8 >= cols
+                        ? kOut
+                        : (gathered ? 0u : (uint32_t)(k + 32 * j) * ld2) + h * 256 + chunk * 16;
+}
+
+// ---- the tile list of the forward product and the input gradient.  Groups
+// are taken from the last to the first (the shared expert, whose tiles are
+// all full, starts first), each as bands of up to kBand row tiles, column tile by
+// column tile.  32 consecutive tiles, one round of an XCD's compute units,
+// go to one XCD: they share a few row and column tiles through its L2.
+constexpr int kBand = 4;
+
+struct TileAt {
+  int g, row0, rows, m0, m_rows, n_tile;
+};
+
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int G, int total, int n_tiles,
+                                          int* tmp, TileAt& t) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+  const int want = (slot >> 5) * 256 + xcd * 32 + (slot & 31);
+  int done = 0;                       // row tiles x column tiles of the groups so far
+  for (int base = 0; base < G; base += kThreads) {
+    const int gi = G - 1 - (base + tid);
     int lo = 0, n = 0;
-    if (gi < G) {
+    if (gi >= 0) {
       lo = clampi(offsets[gi], 0, total);
-      n = clampi(offsets[gi + 1], 0, total) - lo;
-      if (n < 0) n = 0;
+      n = max(clampi(offsets[gi + 1], 0, total) - lo, 0);
     }
-    const int tiles = (n + tile - 1) / tile;
-    s_scan[threadIdx.x] = tiles;
+    const int mt = (n + kTile - 1) / kTile, own = mt * n_tiles;
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 63) tmp[wave] = incl;
     __syncthreads();
-    int before = base, all = base;
-    for (int i = 0; i < kThreads; ++i) {
-      if (i < (int)threadIdx.x) before += s_scan[i];
-      all += s_scan[i];
+    int before = done + incl - own;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) before += tmp[w];
+      done += tmp[w];
+    }
+    if (want >= before && want < before + own) {
+      const int local = want - before;
+      const int band = local / (kBand * n_tiles), in = local - band * kBand * n_tiles;
+      const int height = min(kBand, mt - band * kBand);
+      const int n_tile = in / height, m = band * kBand + in - n_tile * height;
+      const int per = ((n + 15) / 16 + mt - 1) / mt * 16;      // rows of a tile
+      tmp[8] = gi, tmp[9] = lo, tmp[10] = n, tmp[11] = m * per, tmp[12] = n_tile, tmp[13] = per;
     }
     __syncthreads();
-    if (want >= before && want < before + tiles) {
-      s_scan[kThreads] = gi;
-      s_scan[kThreads + 1] = want - before;
-      s_scan[kThreads + 2] = lo;
-      s_scan[kThreads + 3] = n;
+    if (want < done) {
+      t.g = __builtin_amdgcn_readfirstlane(tmp[8]);
+      t.row0 = __builtin_amdgcn_readfirstlane(tmp[9]);
+      t.rows = __builtin_amdgcn_readfirstlane(tmp[10]);
+      t.m0 = __builtin_amdgcn_readfirstlane(tmp[11]);
+      t.n_tile = __builtin_amdgcn_readfirstlane(tmp[12]);
+      t.m_rows = min(__builtin_amdgcn_readfirstlane(tmp[13]), t.rows - t.m0);
+      return t.m_rows > 0;
     }
-    __syncthreads();
-    if (want < all) {
-      g = s_scan[kThreads];
-      m = s_scan[kThreads + 1];
-      row0 = s_scan[kThreads + 2];
-      rows = s_scan[kThreads + 3];
-      return true;
-    }
-    base = all;
   }
   return false;
 }
 
-struct GemmParams {
-  moe_gemm_bf16_args a;
-};
+template <bool KN, int L0, int L1>
+__device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const TileAt& t, uint8_t* smem) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int K = a.k_dim, N = a.n_out, n0 = t.n_tile * kTile;
+  Operand A, B;
+  {
+    // straight A: load j of wave w fills rows 8 (w + 8 j) .. + 7 of a half tile
+    const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
+    long long rows[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = h * 128 + 8 * (wave + 8 * j) + (lane >> 3);
+        rows[h][j] = -1;
+        if (r < t.m_rows) rows[h][j] = a.a_row_index ? clampi(a.a_row_index[t.row0 + t.m0 + r], 0, a.a_rows - 1) : r;
+      }
+    const uint8_t* base = static_cast<const uint8_t*>(a.a);
+    A.base = a.a_row_index ? base : base + (long long)(t.row0 + t.m0) * a.lda * 2;
+    A.bytes = (uint32_t)((a.a_row_index ? a.a_rows : t.m_rows) * a.lda * 2);
+    straight_offsets(A, rows, a.lda, chunk, K);
+  }
+  const uint8_t* b = static_cast<const uint8_t*>(a.b) + (long long)t.g * N * K * 2;
+  if constexpr (KN) {
+    B.base = b + (long long)n0 * 2;
+    B.index = nullptr;
+    B.rows = K;
+    crossed_offsets(B, wave, lane, (uint32_t)N * 2, N - n0, false);
+  } else {
+    const int chunk = (lane & 7) ^ (((lane >> 4) & 1) | ((wave & 3) << 1));
+    long long rows[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = h * 128 + 8 * (wave + 8 * j) + (lane >> 3);
+        rows[h][j] = n0 + r < N ? r : -1;
+      }
+    B.base = b + (long long)n0 * K * 2;
+    B.bytes = (uint32_t)min(kTile, N - n0) * (uint32_t)K * 2;
+    straight_offsets(B, rows, K, chunk, K);
+  }
+  Product<false, KN, false, false, L0, L1> p(smem, wave, lane, (K + kStep - 1) / kStep, A, B);
+  p.run();
 
-__device__ __forceinline__ void store_out(void* out, moe_dtype_t dt, long long at, float v) {
-  if (dt == MOE_F32) static_cast<float*>(out)[at] = v;
-  else static_cast<__bf16*>(out)[at] = (__bf16)v;
+  // A lane holds 4 consecutive columns of one row in each accumulator; with a
+  // straight B its two subtiles make 8 consecutive columns.
+  const int wm = wave & 1, wn = wave >> 1, lk = lane >> 4;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < (h ? L1 : L0); ++i) {
+      const int r = h * 128 + (2 * i + wm) * 16 + (lane & 15);
+      if (r >= t.m_rows) continue;
+      const long long row = t.row0 + t.m0 + r;
+      const float s = a.row_scale ? a.row_scale[row] : 1.0f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int c = n0 + u * 128 + wn * 32 + (KN ? v * 16 + lk * 4 : lk * 8 + v * 4);
+          if (c >= N) continue;
+          const f32x4 x = p.acc[h][i][u][v] * s;
+          if (a.out_dtype == MOE_F32) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + row * a.ldo + c) = x;
+          } else {
+            bf16x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
+            *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + row * a.ldo + c) = y;
+          }
+        }
+    }
 }
 
 template <bool KN>
-__global__ __launch_bounds__(kThreads) void grouped_gemm_bf16_kernel(GemmParams p) {
-  __shared__ __align__(16) uint16_t sa[BM][BK + kPad], sb[BN][BK + kPad];
-  __shared__ int s_scan[kThreads + 4];
-  const moe_gemm_bf16_args& a = p.a;
-  int g, mt, row0, rows;
-  if (!find_row_tile(a.group_offsets, a.num_groups, a.total_rows, BM, blockIdx.x, s_scan, g, mt, row0, rows))
+__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(moe_gemm_bf16_args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  TileAt t;
+  if (!find_tile(a.group_offsets, a.num_groups, a.total_rows, (a.n_out + kTile - 1) / kTile,
+                 reinterpret_cast<int*>(smem), t))
     return;
-  const int m0 = mt * BM, n0 = blockIdx.y * BN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 1, wn = wave >> 1;
-  const uint16_t* A = static_cast<const uint16_t*>(a.a);
-  const uint16_t* B = static_cast<const uint16_t*>(a.b) + (long long)g * a.n_out * a.k_dim;
-  f32x4 acc[4][4] = {};
-  const int K = a.k_dim, N = a.n_out;
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    for (int i = tid; i < BM * BK / 8; i += kThreads) {
-      const int r = i / (BK / 8), c = (i % (BK / 8)) * 8;
-      u32x4 v = {0, 0, 0, 0};
-      if (m0 + r < rows && k0 + c < K) {
-        int src = row0 + m0 + r;
-        if (a.a_row_index) src = a.a_row_index[src];
-        src = clampi(src, 0, a.a_rows - 1);
-        v = *reinterpret_cast<const u32x4*>(A + (long long)src * a.lda + k0 + c);
-      }
-      *reinterpret_cast<u32x4*>(&sa[r][c]) = v;
-    }
-    if constexpr (!KN) {
-      for (int i = tid; i < BN * BK / 8; i += kThreads) {
-        const int r = i / (BK / 8), c = (i % (BK / 8)) * 8;
-        u32x4 v = {0, 0, 0, 0};
-        if (n0 + r < N && k0 + c < K) v = *reinterpret_cast<const u32x4*>(B + (long long)(n0 + r) * K + k0 + c);
-        *reinterpret_cast<u32x4*>(&sb[r][c]) = v;
-      }
-    } else {
-      for (int i = tid; i < BK * BN / 8; i += kThreads) {
-        const int r = i / (BN / 8), c = (i % (BN / 8)) * 8;
-        u32x4 v = {0, 0, 0, 0};
-        if (k0 + r < K && n0 + c < N) v = *reinterpret_cast<const u32x4*>(B + (long long)(k0 + r) * N + n0 + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sb[c + j][r] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
-      }
-    }
-    __syncthreads();
-    bf16x8 fa[4], fb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fa[i] = *reinterpret_cast<const bf16x8*>(&sa[wm * 64 + i * 16 + (lane & 15)][(lane >> 4) * 8]);
-      fb[i] = *reinterpret_cast<const bf16x8*>(&sb[wn * 64 + i * 16 + (lane & 15)][(lane >> 4) * 8]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int r = m0 + wm * 64 + i * 16 + (lane >> 4) * 4 + v;
-      if (r < rows) {
-        const float s = a.row_scale ? a.row_scale[row0 + r] : 1.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = n0 + wn * 64 + j * 16 + (lane & 15);
-          if (c < N) store_out(a.out, a.out_dtype, (long long)(row0 + r) * a.ldo + c, acc[i][j][v] * s);
-        }
-      }
-    }
+  __syncthreads();        // the list's scratch becomes the first half tile
+  const int subtiles = (t.m_rows + 15) / 16;
+  const int l0 = min((subtiles + 1) / 2, 4), l1 = max((subtiles - 8 + 1) / 2, 0);
+  if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(a, t, smem) : gemm_tile<KN, 4, 3>(a, t, smem);
+  else if (l1 > 0) l1 > 1 ? gemm_tile<KN, 4, 2>(a, t, smem) : gemm_tile<KN, 4, 1>(a, t, smem);
+  else if (l0 > 2) l0 > 3 ? gemm_tile<KN, 4, 0>(a, t, smem) : gemm_tile<KN, 3, 0>(a, t, smem);
+  else l0 > 1 ? gemm_tile<KN, 2, 0>(a, t, smem) : gemm_tile<KN, 1, 0>(a, t, smem);
 }
 
-__global__ __launch_bounds__(kThreads) void grouped_wgrad_bf16_kernel(moe_wgrad_bf16_args a) {
-  __shared__ __align__(16) uint16_t sa[BM][BK + kPad], sb[BN][BK + kPad];
-  const int g = blockIdx.z;
+// ---- weight gradient: one workgroup per 256 x 256 tile of one group's dW.
+template <bool A_G, bool B_G>
+__global__ __launch_bounds__(kThreads, 2) void grouped_wgrad_bf16_kernel(moe_wgrad_bf16_args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int nt = (a.n + kTile - 1) / kTile, kt = (a.k + kTile - 1) / kTile;
+  const int g = blockIdx.x / (nt * kt), in = blockIdx.x - g * nt * kt;
+  const int m0 = in / kt * kTile, n0 = in % kt * kTile;
   const int row0 = clampi(a.group_offsets[g], 0, a.total_rows);
-  const int end = clampi(a.group_offsets[g + 1], 0, a.total_rows);
-  const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 1, wn = wave >> 1;
-  const uint16_t* A = static_cast<const uint16_t*>(a.a);
-  const uint16_t* B = static_cast<const uint16_t*>(a.b);
-  f32x4 acc[4][4] = {};
-  for (int r0 = row0; r0 < end; r0 += BK) {
-    for (int i = tid; i < BK * BM / 8; i += kThreads) {
-      const int r = i / (BM / 8), c = (i % (BM / 8)) * 8;
-      u32x4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-      if (r0 + r < end) {
-        int ra = r0 + r, rb = r0 + r;
-        if (a.a_row_index) ra = a.a_row_index[ra];
-        if (a.b_row_index) rb = a.b_row_index[rb];
-        ra = clampi(ra, 0, a.a_rows - 1);
-        rb = clampi(rb, 0, a.b_rows - 1);
-        if (m0 + c < a.n) va = *reinterpret_cast<const u32x4*>(A + (long long)ra * a.lda + m0 + c);
-        if (n0 + c < a.k) vb = *reinterpret_cast<const u32x4*>(B + (long long)rb * a.ldb + n0 + c);
-      }
+  const int rows = max(clampi(a.group_offsets[g + 1], 0, a.total_rows) - row0, 0);
+  Operand A, B;
+  const uint8_t* ab = static_cast<const uint8_t*>(a.a) + (long long)m0 * 2;
+  const uint8_t* bb = static_cast<const uint8_t*>(a.b) + (long long)n0 * 2;
+  A.base = A_G ? ab : ab + (long long)row0 * a.lda * 2;
+  B.base = B_G ? bb : bb + (long long)row0 * a.ldb * 2;
+  A.bytes = (uint32_t)(a.a_rows * a.lda * 2 - m0 * 2);
+  B.bytes = (uint32_t)(a.b_rows * a.ldb * 2 - n0 * 2);
+  A.index = A_G ? a.a_row_index + row0 : nullptr;
+  B.index = B_G ? a.b_row_index + row0 : nullptr;
+  A.rows = B.rows = rows;
+  A.max_row = a.a_rows - 1;
+  B.max_row = a.b_rows - 1;
+  crossed_offsets(A, wave, lane, (uint32_t)a.lda * 2, a.n - m0, A_G);
+  crossed_offsets(B, wave, lane, (uint32_t)a.ldb * 2, a.k - n0, B_G);
+  Product<true, true, A_G, B_G, 4, 4> p(smem, wave, lane, (rows + kStep - 1) / kStep, A, B);
+  p.run();
+
+  const int wm = wave & 1, wn = wave >> 1, lk = lane >> 4;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sa[c + j][r] = (uint16_t)(va[j >> 1] >> (16 * (j & 1)));
-        sb[c + j][r] = (uint16_t)(vb[j >> 1] >> (16 * (j & 1)));
-      }
-    }
-    __syncthreads();
-    bf16x8 fa[4], fb[4];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      fa[i] = *reinterpret_cast<const bf16x8*>(&sa[wm * 64 + i * 16 + (lane & 15)][(lane >> 4) * 8]);
-      fb[i] = *reinterpret_cast<const bf16x8*>(&sb[wn * 64 + i * 16 + (lane & 15)][(lane >> 4) * 8]);
-    }
+      const int r = m0 + h * 128 + (2 * i + wm) * 16 + (lane & 15);
+      if (r >= a.n) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    __syncthreads();
-  }
+        for (int v = 0; v < 2; ++v) {
+          const int c = n0 + u * 128 + wn * 32 + v * 16 + lk * 4;
+          if (c >= a.k) continue;
+          const long long at = ((long long)g * a.n + r) * a.k + c;
+          f32x4 x = p.acc[h][i][u][v];
+          if (a.out_dtype == MOE_F32) {
+            f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at);
+            *o = a.accumulate ? x + *o : x;
+          } else {
+            bf16x4* o = reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at);
+            if (a.accumulate) {
+              const bf16x4 old = *o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+              for (int e = 0; e < 4; ++e) x[e] += (float)old[e];
+            }
+            bf16x4 y;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int r = m0 + wm * 64 + i * 16 + (lane >> 4) * 4 + v;
-      if (r < a.n) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = n0 + wn * 64 + j * 16 + (lane & 15);
-          if (c < a.k) {
-            const long long at = ((long long)g * a.n + r) * a.k + c;
-            float t = acc[i][j][v];
-            if (a.accumulate)
-              t += a.out_dtype == MOE_F32 ? static_cast<const float*>(a.out)[at]
-                                          : (float)static_cast<const __bf16*>(a.out)[at];
-            store_out(a.out, a.out_dtype, at, t);
+            for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
+            *o = y;
           }
         }
-      }
     }
 }
 
 bool valid_dt(moe_dtype_t d) { return d == MOE_BF16 || d == MOE_F32; }
 // element rows that 32-bit byte offsets of a gathered operand can reach
 bool fits31(long long rows, long long ld) { return rows * ld * 2 < (1LL << 31); }
+// a tile's or a step's rows of an operand that is not gathered
+bool tile_fits31(long long ld) { return fits31(kTile, ld); }
 
 }  // namespace
 
@@ -222,22 +553,25 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hi
     return MOE_ERR_SHAPE;
   if (a.num_groups > kMaxGroups || !valid_dt(a.out_dtype) ||
       (a.b_layout != MOE_B_NK && a.b_layout != MOE_B_KN) ||
-      (long long)a.n_out * a.k_dim * 2 >= (1LL << 31))
+      (long long)a.n_out * a.k_dim * 2 >= (1LL << 31) || !tile_fits31(a.lda))
     return MOE_ERR_UNSUPPORTED;
-  if (a.a_row_index ? !fits31(a.a_rows, a.lda) : a.a_rows < a.total_rows)
-    return a.a_row_index ? MOE_ERR_UNSUPPORTED : MOE_ERR_SHAPE;
+  if (a.a_row_index && !fits31(a.a_rows, a.lda)) return MOE_ERR_UNSUPPORTED;
+  if (!a.a_row_index && a.a_rows < a.total_rows) return MOE_ERR_SHAPE;
   if (a.total_rows == 0 || a.n_out == 0) return MOE_OK;
   if (a.a_rows == 0) return MOE_ERR_SHAPE;
   if (!a.group_offsets || !a.out || (a.k_dim > 0 && (!a.a || !a.b))) return MOE_ERR_NULL;
   if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.out)) return MOE_ERR_ALIGN;
+  const long long tiles = ((long long)a.total_rows / kTile +
+                           (a.num_groups < a.total_rows ? a.num_groups : a.total_rows)) *
+                          ((a.n_out + kTile - 1) / kTile);
+  const long long grid = (tiles + 255) / 256 * 256;
+  if (grid > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
   if (moe_status_t s = check_device()) return s;
-  GemmParams p{a};
-  const long long tiles = (long long)a.total_rows / BM + (a.num_groups < a.total_rows ? a.num_groups : a.total_rows);
-  const dim3 grid((unsigned)tiles, (unsigned)((a.n_out + BN - 1) / BN));
-  if (a.b_layout == MOE_B_NK)
-    hipLaunchKernelGGL(grouped_gemm_bf16_kernel<false>, grid, dim3(kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL(grouped_gemm_bf16_kernel<true>, grid, dim3(kThreads), 0, stream, p);
+  const bool kn = a.b_layout == MOE_B_KN;
+  auto kernel = kn ? grouped_gemm_bf16_kernel<true> : grouped_gemm_bf16_kernel<false>;
+  static std::atomic<uint64_t> lds_set[2] = {};
+  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set[kn])) return st;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), kLds, stream, a);
   return launch_status();
 }
 
@@ -254,7 +588,8 @@ extern "C" moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, 
       a.lda < a.n || a.lda % 8 || a.ldb < a.k || a.ldb % 8 || a.a_rows < 0 || a.b_rows < 0)
     return MOE_ERR_SHAPE;
   if (a.num_groups > kMaxGroups || !valid_dt(a.out_dtype)) return MOE_ERR_UNSUPPORTED;
-  if ((a.a_row_index && !fits31(a.a_rows, a.lda)) || (a.b_row_index && !fits31(a.b_rows, a.ldb)))
+  if ((a.a_row_index && !fits31(a.a_rows, a.lda)) || (a.b_row_index && !fits31(a.b_rows, a.ldb)) ||
+      !tile_fits31(a.lda) || !tile_fits31(a.ldb))
     return MOE_ERR_UNSUPPORTED;
   if ((!a.a_row_index && a.a_rows < a.total_rows) || (!a.b_row_index && a.b_rows < a.total_rows) ||
       (a.total_rows > 0 && (a.a_rows == 0 || a.b_rows == 0)))
@@ -264,8 +599,16 @@ extern "C" moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, 
   if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.out)) return MOE_ERR_ALIGN;
   if (ws_bytes < moe_grouped_wgrad_bf16_workspace_bytes(a.num_groups, a.total_rows, a.n, a.k))
     return MOE_ERR_WORKSPACE;
+  const long long tiles = (long long)a.num_groups * ((a.n + kTile - 1) / kTile) * ((a.k + kTile - 1) / kTile);
+  if (tiles > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
   if (moe_status_t s = check_device()) return s;
-  const dim3 grid((unsigned)((a.n + BM - 1) / BM), (unsigned)((a.k + BN - 1) / BN), (unsigned)a.num_groups);
-  hipLaunchKernelGGL(grouped_wgrad_bf16_kernel, grid, dim3(kThreads), 0, stream, a);
+  static void (*const table[2][2])(moe_wgrad_bf16_args) = {
+      {grouped_wgrad_bf16_kernel<false, false>, grouped_wgrad_bf16_kernel<false, true>},
+      {grouped_wgrad_bf16_kernel<true, false>, grouped_wgrad_bf16_kernel<true, true>}};
+  const int ga = a.a_row_index != nullptr, gb = a.b_row_index != nullptr;
+  static std::atomic<uint64_t> lds_set[2][2] = {};
+  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(table[ga][gb]), kLds, lds_set[ga][gb]))
+    return st;
+  hipLaunchKernelGGL(table[ga][gb], dim3((unsigned)tiles), dim3(kThreads), kLds, stream, a);
   return launch_status();
 }
