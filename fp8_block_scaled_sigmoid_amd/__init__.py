@@ -573,24 +573,32 @@ def _dtype_code(t, name):
     return _DT[t.dtype]
 
 
-def _rows(t, shape, dtype, name):
+def _rows(t, rows, cols, dtype, name):
     """A device matrix whose rows are contiguous; returns (pointer, row stride)."""
     if t is None:
         return None, 0
-    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape)
-            and (t.stride(1) == 1 or t.shape[1] <= 1)):
-        raise ValueError(f"{name}: need a {dtype} device tensor {tuple(shape)} with contiguous "
-                         f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dtype is dtype and t.is_cuda and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step == 1 or cols <= 1:
+            return t.data_ptr(), ld if rows > 1 else cols
+    raise ValueError(f"{name}: need a {dtype} device tensor {(rows, cols)} with contiguous "
+                     f"rows, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
 
 
 def _vector(t, n, name, dtype=torch.float32):
     if t is None:
         return None
-    if not (t.is_cuda and t.dtype == dtype and t.numel() == n and t.is_contiguous()):
-        raise ValueError(f"{name}: need {n} contiguous {dtype} values on the device, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: need {n} contiguous {dtype} values on the device, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _queue(stream):
+    """The stream's handle (the current stream's without one)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _gate(gate, T, H, b_dtype):
@@ -601,7 +609,7 @@ def _gate(gate, T, H, b_dtype):
         return MOE_GATE_CHANNEL, _vector(gate, H, "gate"), 0
     if tuple(gate.shape) == (T, 1):
         return MOE_GATE_TOKEN, _vector(gate, T, "gate"), 0
-    return (MOE_GATE_FULL, *_rows(gate, (T, H), b_dtype, "gate"))
+    return (MOE_GATE_FULL, *_rows(gate, T, H, b_dtype, "gate"))
 
 
 def moe_block_norm(x, b=None, w_pre=None, w_post=None, gate=None, alpha=1.0, beta=1.0, eps=1e-6,
@@ -626,11 +634,11 @@ def moe_block_norm(x, b=None, w_pre=None, w_post=None, gate=None, alpha=1.0, bet
     if h is None and w_pre is not None:
         h = torch.empty(T, H, dtype=bt, device=x.device)
     mode, gp, ldg = _gate(gate, T, H, bt)
-    a = BlockNormArgs(T, H, xdt, _DT.get(bt, -1), *_rows(x, (T, H), x.dtype, "x"),
-                      *_rows(b, (T, H), bt, "b"), _vector(w_pre, H, "w_pre"),
+    a = BlockNormArgs(T, H, xdt, _DT.get(bt, -1), *_rows(x, T, H, x.dtype, "x"),
+                      *_rows(b, T, H, bt, "b"), _vector(w_pre, H, "w_pre"),
                       _vector(w_post, H, "w_post"), mode, gp, ldg, alpha, beta, eps,
-                      *_rows(r, (T, H), x.dtype, "r"), *_rows(h, (T, H), bt, "h"))
-    _check("moe_block_norm", lib().moe_block_norm(ctypes.byref(a), _stream(stream)))
+                      *_rows(r, T, H, x.dtype, "r"), *_rows(h, T, H, bt, "h"))
+    _check("moe_block_norm", lib().moe_block_norm(ctypes.byref(a), _queue(stream)))
     return (x if b is None else r), h
 
 
@@ -669,17 +677,17 @@ def moe_block_norm_backward(r, dr=None, dh=None, b=None, w_pre=None, w_post=None
         ws = torch.empty(max(moe_block_norm_backward_workspace_bytes(T, H), 16), dtype=torch.uint8,
                          device=dev)
     if mode == MOE_GATE_FULL:
-        dgp, lddg = _rows(dgate, (T, H), bt, "dgate")
+        dgp, lddg = _rows(dgate, T, H, bt, "dgate")
     else:
         dgp, lddg = _vector(dgate, H if mode == MOE_GATE_CHANNEL else T, "dgate"), 0
-    a = BlockNormBwdArgs(T, H, _dtype_code(r, "r"), _DT.get(bt, -1), *_rows(r, (T, H), r.dtype, "r"),
-                         *_rows(dr, (T, H), r.dtype, "dr"), *_rows(dh, (T, H), bt, "dh"),
-                         *_rows(b, (T, H), bt, "b"), _vector(w_pre, H, "w_pre"),
+    a = BlockNormBwdArgs(T, H, _dtype_code(r, "r"), _DT.get(bt, -1), *_rows(r, T, H, r.dtype, "r"),
+                         *_rows(dr, T, H, r.dtype, "dr"), *_rows(dh, T, H, bt, "dh"),
+                         *_rows(b, T, H, bt, "b"), _vector(w_pre, H, "w_pre"),
                          _vector(w_post, H, "w_post"), mode, gp, ldg, alpha, beta, eps,
-                         *_rows(dx, (T, H), r.dtype, "dx"), *_rows(db, (T, H), bt, "db"),
+                         *_rows(dx, T, H, r.dtype, "dx"), *_rows(db, T, H, bt, "db"),
                          _vector(dw_pre, H, "dw_pre"), _vector(dw_post, H, "dw_post"), dgp, lddg)
     _check("moe_block_norm_backward", lib().moe_block_norm_backward(
-        ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)))
+        ctypes.byref(a), _ptr(ws), ws.numel(), _queue(stream)))
     return dx, db, dw_pre, dw_post, dgate
 
 
@@ -697,14 +705,14 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
         raise ValueError(f"group_offsets: need {G + 1} values")
     if out is None:
         out = torch.empty(total_rows, n, dtype=out_dtype, device=a.device)
-    ap, lda = _rows(a, (a.shape[0], K), torch.bfloat16, "a")
-    op, ldo = _rows(out, (total_rows, n), out.dtype, "out")
+    ap, lda = _rows(a, a.shape[0], K, torch.bfloat16, "a")
+    op, ldo = _rows(out, total_rows, n, out.dtype, "out")
     args = GemmBf16Args(ap, lda, a.shape[0],
                         _vector(a_row_index, total_rows, "a_row_index", torch.int32),
                         b.data_ptr(), MOE_B_KN if b_kn else MOE_B_NK, group_offsets.data_ptr(), G,
                         total_rows, n, K, _dtype_code(out, "out"), op, ldo,
                         _vector(row_scale, total_rows, "row_scale"))
-    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(ctypes.byref(args), _stream(stream)))
+    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(ctypes.byref(args), _queue(stream)))
     return out
 
 
@@ -729,8 +737,8 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
     if tuple(out.shape) != (G, n, k):
         raise ValueError(f"out: need [{G}, {n}, {k}], got {tuple(out.shape)}")
     _dev(out, out.dtype, "out")
-    ap, lda = _rows(a, (a.shape[0], n), torch.bfloat16, "a")
-    bp, ldb = _rows(b, (b.shape[0], k), torch.bfloat16, "b")
+    ap, lda = _rows(a, a.shape[0], n, torch.bfloat16, "a")
+    bp, ldb = _rows(b, b.shape[0], k, torch.bfloat16, "b")
     need = moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k)
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=a.device)
@@ -741,7 +749,7 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
                          group_offsets.data_ptr(), G, total_rows, n, k, _dtype_code(out, "out"),
                          out.data_ptr(), 1 if accumulate else 0)
     _check("moe_grouped_wgrad_bf16", lib().moe_grouped_wgrad_bf16(
-        ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _queue(stream)))
     return out
 
 
@@ -751,10 +759,10 @@ def moe_swiglu(a, h=None, stream=None):
     if a.shape[1] % 2:
         raise ValueError("a: need an even number of columns (gate columns, then up columns)")
     h = torch.empty(R, I, dtype=a.dtype, device=a.device) if h is None else h
-    ap, lda = _rows(a, (R, 2 * I), a.dtype, "a")
-    hp, ldh = _rows(h, (R, I), a.dtype, "h")
+    ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
+    hp, ldh = _rows(h, R, I, a.dtype, "h")
     _check("moe_swiglu", lib().moe_swiglu(ap, _dtype_code(a, "a"), R, I, lda, hp, ldh,
-                                          _stream(stream)))
+                                          _queue(stream)))
     return h
 
 
@@ -770,13 +778,13 @@ def moe_swiglu_backward(a, dh, row_gate=None, da=None, dgate=None, hg=None, stre
     dgate = torch.empty(R, dtype=torch.float32, device=a.device) if dgate is None else dgate
     hg = torch.empty(R, I, dtype=a.dtype, device=a.device) if hg is None else hg
     dgate, hg = (None if t is False else t for t in (dgate, hg))
-    ap, lda = _rows(a, (R, 2 * I), a.dtype, "a")
-    dhp, lddh = _rows(dh, (R, I), a.dtype, "dh")
-    dap, ldda = _rows(da, (R, 2 * I), a.dtype, "da")
-    hgp, ldhg = _rows(hg, (R, I), a.dtype, "hg")
+    ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
+    dhp, lddh = _rows(dh, R, I, a.dtype, "dh")
+    dap, ldda = _rows(da, R, 2 * I, a.dtype, "da")
+    hgp, ldhg = _rows(hg, R, I, a.dtype, "hg")
     _check("moe_swiglu_backward", lib().moe_swiglu_backward(
         ap, dhp, dt, R, I, lda, lddh, _vector(row_gate, R, "row_gate"), dap, ldda,
-        _vector(dgate, R, "dgate"), hgp, ldhg, _stream(stream)))
+        _vector(dgate, R, "dgate"), hgp, ldhg, _queue(stream)))
     return da, dgate, hg
 
 
@@ -840,7 +848,7 @@ def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
     norm = torch.empty(1, dtype=torch.float32, device=grads.device) if norm is None else norm
     _check("moe_grad_norm", lib().moe_grad_norm(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
-        _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), _stream(stream)))
+        _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), _queue(stream)))
     return sumsq, norm
 
 
@@ -850,7 +858,7 @@ def moe_grad_scale(grads, sumsq, max_norm, result=None, stream=None):
     result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
     _check("moe_grad_scale", lib().moe_grad_scale(
         _ptr(grads.table), grads.n, grads.chunks, _vector(sumsq, 1, "sumsq", torch.float64),
-        float(max_norm), _vector(result, 2, "result"), _stream(stream)))
+        float(max_norm), _vector(result, 2, "result"), _queue(stream)))
     return result
 
 
@@ -861,7 +869,7 @@ def moe_grad_clip(grads, max_norm, result=None, stream=None):
     result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
     _check("moe_grad_clip", lib().moe_grad_clip(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
-        float(max_norm), _vector(result, 2, "result"), _stream(stream)))
+        float(max_norm), _vector(result, 2, "result"), _queue(stream)))
     return result
 
 

@@ -13,6 +13,8 @@
 //   over what the gate is shared by)
 // Both statistics come from the rows themselves, so nothing but r and b has to
 // be kept between the passes.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace {
@@ -20,21 +22,23 @@ namespace {
 using namespace moe;
 
 constexpr int kMaxWaves = 16;
-constexpr int kMaxThreads = kMaxWaves * 64;
-constexpr int kMaxWidth = kMaxThreads * 16;   // two vectors of 8 a thread
+constexpr int kMaxWidth = 16384;
+constexpr int kFwdWaves = 8, kBwdWaves = 16;      // waves of a workgroup
 
 // How rows are laid over threads: `wpr` waves share a row, a workgroup holds
-// `groups` rows at a time, and a thread owns vectors t, t + 64 wpr of its row.
+// `groups` rows at a time, and a thread owns vectors t, t + 64 wpr, ... of its
+// row, `items` of them.
 struct RowShape {
   int wpr, groups, items;
 };
 
-RowShape row_shape(int H) {
+RowShape row_shape(int H, int waves) {
   RowShape s;
   const int vecs = (H + 7) / 8;
-  s.items = vecs > kMaxThreads ? 2 : 1;
+  s.items = 1;
+  while (vecs > waves * 64 * s.items) s.items *= 2;
   s.wpr = (vecs + 64 * s.items - 1) / (64 * s.items);
-  s.groups = kMaxWaves / s.wpr;
+  s.groups = waves / s.wpr;
   return s;
 }
 
@@ -64,7 +68,7 @@ struct FwdParams {
 };
 
 template <typename X, typename B, int ITEMS>
-__global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(FwdParams p) {
+__global__ __launch_bounds__(kFwdWaves * 64) void block_norm_kernel(FwdParams p) {
   // one buffer per reduction and row parity: a row's sums are read behind its
   // own barrier, and the buffer is written again two barriers later
   __shared__ float red_b[2][1][kMaxWaves], red_r[2][1][kMaxWaves];
@@ -174,17 +178,21 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_kernel(FwdParams p) {
 // ---- backward
 
 // Rows are handed out block by block (a persistent grid), so that each
-// thread keeps the running sums of its channels' dw_pre, dw_post and dgate in
-// registers over all its rows; a second kernel adds the workgroups' partial
-// sums in workgroup order.
+// thread keeps the running sums of its channels in registers over all its
+// rows; a second kernel adds the workgroups' partial sums in workgroup order.
+// Two sums serve all three gradients: dw_pre, and S = sum_t d b^ times a
+// per-row gate, from which dw_post = beta gate_c S and, for a gate per channel,
+// dgate = beta w_post S.  A row's four inputs are read once, the next row's
+// while one is worked on; rows wider than 8192 do not fit the registers, and
+// read theirs again after the first reduction instead (from L2).
 struct BwdParams {
   moe_block_norm_bwd_args a;
   int wpr, groups;
-  float* part;      // [3][blocks * groups][H]: dw_pre, dw_post, dgate
+  float* part;      // [3][blocks][H]: dw_pre, dw_post, dgate
 };
 
-template <typename X, typename B, int ITEMS>
-__global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_kernel(BwdParams p) {
+template <typename X, typename B, int ITEMS, bool FULL>
+__global__ __launch_bounds__(kBwdWaves * 64) void block_norm_bwd_kernel(BwdParams p) {
   __shared__ float red_a[2][3][kMaxWaves], red_c[2][1][kMaxWaves];   // by row parity, as above
   int par = 0;
   const moe_block_norm_bwd_args& a = p.a;
@@ -195,58 +203,78 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_kernel(BwdParams p
   const int H = a.H;
   const float inv_h = 1.0f / (float)H;
   const bool has_b = a.b != nullptr, post = has_b && a.w_post;
+  const bool channel = a.gate_mode == MOE_GATE_CHANNEL, token = a.gate_mode == MOE_GATE_TOKEN;
+  constexpr bool kHold = ITEMS == 1, kAhead = kHold && !FULL;      // as registers allow
 
-  float acc_pre[ITEMS][8] = {}, acc_post[ITEMS][8] = {}, acc_gate[ITEMS][8] = {};
-  float w_pre[ITEMS][8] = {}, w_post[ITEMS][8], gate_c[ITEMS][8];
+  // w_pre, and w_n = beta w_post (gate per channel): u = w_n (gate of the row) d
+  float w_pre[ITEMS][8] = {}, w_n[ITEMS][8] = {}, acc_pre[ITEMS][8] = {}, acc_b[ITEMS][8] = {};
+  auto load_w = [&](const void* w, int c, float (&f)[8]) {
+    Vec8<float> v;
+    v.load(static_cast<const float*>(w) + c, H - c);
+    v.get(f);
+  };
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c = (gt + i * stride) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w_post[i][j] = gate_c[i][j] = 1.0f;
     if (c < H) {
-      Vec8<float> w;
-      if (a.dh) {
-        w.load(a.w_pre + c, H - c);
-        w.get(w_pre[i]);
-      }
+      float f[8];
+      if (a.dh) load_w(a.w_pre, c, w_pre[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w_n[i][j] = a.beta;
       if (post) {
-        w.load(a.w_post + c, H - c);
-        w.get(w_post[i]);
+        load_w(a.w_post, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w_n[i][j] *= f[j];
       }
-      if (a.gate_mode == MOE_GATE_CHANNEL) {
-        w.load(static_cast<const float*>(a.gate) + c, H - c);
-        w.get(gate_c[i]);
+      if (channel) {
+        load_w(a.gate, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w_n[i][j] *= f[j];
       }
     }
   }
 
+  struct Row {
+    Vec8<X> r, dr;
+    Vec8<B> b, dh, g;
+  };
+  auto load_b = [&](int row, int c, Row& v) {
+    v.b.zero();
+    if (has_b && row < a.T && c < H)
+      v.b.load(static_cast<const B*>(a.b) + (long long)row * a.ldb + c, H - c);
+  };
+  auto load = [&](int row, int i, Row& v) {
+    const int c = (gt + i * stride) * 8;
+    v.r.zero(), v.dr.zero(), v.dh.zero(), v.g.zero();
+    if (row < a.T && c < H) {
+      if (a.dh) {
+        v.r.load(static_cast<const X*>(a.r) + (long long)row * a.ldr + c, H - c);
+        v.dh.load(static_cast<const B*>(a.dh) + (long long)row * a.lddh + c, H - c);
+      }
+      if (a.dr) v.dr.load(static_cast<const X*>(a.dr) + (long long)row * a.lddr + c, H - c);
+      if (FULL) v.g.load(static_cast<const B*>(a.gate) + (long long)row * a.ldg + c, H - c);
+    }
+    load_b(row, c, v);
+  };
+
+  Row cur, next;
+  if (kAhead) load(blockIdx.x * p.groups + grp, 0, next);
   for (int row0 = blockIdx.x * p.groups; row0 < a.T; row0 += gridDim.x * p.groups, par ^= 1) {
     const int row = row0 + grp;
     const bool live = row < a.T;
-    Vec8<X> rv[ITEMS], drv[ITEMS];
-    Vec8<B> bv[ITEMS], dhv[ITEMS], gv[ITEMS];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int c = (gt + i * stride) * 8;
-      rv[i].zero(), drv[i].zero(), bv[i].zero(), dhv[i].zero(), gv[i].zero();
-      if (live && c < H) {
-        if (a.dh) {
-          rv[i].load(static_cast<const X*>(a.r) + (long long)row * a.ldr + c, H - c);
-          dhv[i].load(static_cast<const B*>(a.dh) + (long long)row * a.lddh + c, H - c);
-        }
-        if (a.dr) drv[i].load(static_cast<const X*>(a.dr) + (long long)row * a.lddr + c, H - c);
-        if (has_b) bv[i].load(static_cast<const B*>(a.b) + (long long)row * a.ldb + c, H - c);
-        if (a.gate_mode == MOE_GATE_FULL)
-          gv[i].load(static_cast<const B*>(a.gate) + (long long)row * a.ldg + c, H - c);
-      }
+    if (kAhead) {
+      cur = next;
+      load(row + gridDim.x * p.groups, 0, next);
+    } else if (kHold) {
+      load(row, 0, cur);
     }
-    const float gate_t =
-        live && a.gate_mode == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    const float gate_t = live && token ? static_cast<const float*>(a.gate)[row] : 1.0f;
     float s[3] = {0.0f, 0.0f, 0.0f};       // r^2, dh w_pre r, b^2
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
+      if (!kHold) load(row, i, cur);
       float r[8], dh[8], b[8];
-      rv[i].get(r), dhv[i].get(dh), bv[i].get(b);
+      cur.r.get(r), cur.dh.get(dh), cur.b.get(b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         s[0] = __builtin_fmaf(r[j], r[j], s[0]);
@@ -258,82 +286,105 @@ __global__ __launch_bounds__(kMaxThreads) void block_norm_bwd_kernel(BwdParams p
     const float inv_r = 1.0f / __builtin_sqrtf(s[0] * inv_h + a.eps);
     const float inv_b = post ? 1.0f / __builtin_sqrtf(s[2] * inv_h + a.eps) : 1.0f;
     const float m_r = s[1] * inv_r * inv_h;      // mean(v r^)
-    float d[ITEMS][8], t3[1] = {0.0f};           // t3: sum of u b^ (before a token gate)
+    float u[ITEMS][8], t[1] = {0.0f};            // t: sum of u b^ (before a token's gate)
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = (gt + i * stride) * 8;
-      float r[8], dh[8], b[8];
-      rv[i].get(r), dhv[i].get(dh), bv[i].get(b), drv[i].get(d[i]);
+      if (!kHold) load(row, i, cur);
+      float r[8], dh[8], d[8];
+      cur.r.get(r), cur.dh.get(dh), cur.dr.get(d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float rh = r[j] * inv_r;
         acc_pre[i][j] = __builtin_fmaf(dh[j], rh, acc_pre[i][j]);
-        d[i][j] += inv_r * (dh[j] * w_pre[i][j] - rh * m_r);
+        d[j] += inv_r * (dh[j] * w_pre[i][j] - rh * m_r);
       }
       if (a.dx && live && c < H) {
         float dx[8];
         const float al = has_b ? a.alpha : 1.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] = al * d[i][j];
+        for (int j = 0; j < 8; ++j) dx[j] = al * d[j];
         Vec8<X>::store(static_cast<X*>(a.dx) + (long long)row * a.lddx + c, dx, H - c);
       }
       if (has_b) {
-        float g[8], dg[8];
-        gv[i].get(g);
+        float b[8], g[8], dg[8];
+        cur.b.get(b), cur.g.get(g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float bh = b[j] * inv_b, dn0 = a.beta * d[i][j], n = bh * w_post[i][j];
-          const float gj = a.gate_mode == MOE_GATE_FULL ? g[j] : gate_c[i][j];
-          dg[j] = dn0 * n;
-          acc_gate[i][j] += dg[j];
-          t3[0] = __builtin_fmaf(dg[j], gj, t3[0]);
-          acc_post[i][j] = __builtin_fmaf(dn0 * gj * gate_t, bh, acc_post[i][j]);
-          d[i][j] = dn0 * gj * gate_t * w_post[i][j];     // u
+          const float db = d[j] * (b[j] * inv_b), gj = FULL ? g[j] : gate_t;
+          dg[j] = db * w_n[i][j];
+          acc_b[i][j] = __builtin_fmaf(db, gj, acc_b[i][j]);
+          t[0] = FULL ? __builtin_fmaf(dg[j], gj, t[0]) : t[0] + dg[j];
+          u[i][j] = d[j] * w_n[i][j] * gj;
         }
-        if (a.gate_mode == MOE_GATE_FULL && a.dgate && live && c < H)
+        if (FULL && a.dgate && live && c < H)
           Vec8<B>::store(static_cast<B*>(a.dgate) + (long long)row * a.lddg + c, dg, H - c);
       }
     }
     if (!has_b) continue;
-    if (post || a.gate_mode == MOE_GATE_TOKEN) row_sums(t3, red_c[par], wave, lane, first_wave, p.wpr);
-    if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && live && gt == 0)
-      static_cast<float*>(a.dgate)[row] = t3[0];
-    const float m_b = post ? t3[0] * gate_t * inv_h : 0.0f;     // mean(u b^)
+    if (post || token) row_sums(t, red_c[par], wave, lane, first_wave, p.wpr);
+    if (token && a.dgate && live && gt == 0) static_cast<float*>(a.dgate)[row] = t[0];
+    const float m_b = post ? t[0] * gate_t * inv_h : 0.0f;     // mean(u b^)
     if (a.db && live) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i) {
         const int c = (gt + i * stride) * 8;
         if (c < H) {
+          if (!kHold) load_b(row, c, cur);
           float b[8];
-          bv[i].get(b);
+          cur.b.get(b);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[i][j] = inv_b * (d[i][j] - b[j] * inv_b * m_b);
-          Vec8<B>::store(static_cast<B*>(a.db) + (long long)row * a.lddb + c, d[i], H - c);
+          for (int j = 0; j < 8; ++j) u[i][j] = inv_b * (u[i][j] - b[j] * inv_b * m_b);
+          Vec8<B>::store(static_cast<B*>(a.db) + (long long)row * a.lddb + c, u[i], H - c);
         }
       }
     }
   }
 
-  const long long slot = (long long)blockIdx.x * p.groups + grp;
-  const long long plane = (long long)gridDim.x * p.groups * H;
+  // The groups' sums are joined in LDS, one plane at a time, then written.
+  extern __shared__ float join[];      // [groups - 1][H] when there are several groups
+  auto finish = [&](float (&acc)[ITEMS][8], int plane, const float* w, float k) {
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int c = (gt + i * stride) * 8;
-    if (c < H) {
-      float* o = p.part + slot * H + c;
-      if (a.dw_pre) Vec8<float>::store(o, acc_pre[i], H - c);
-      if (a.dw_post) Vec8<float>::store(o + plane, acc_post[i], H - c);
-      if (a.dgate && a.gate_mode == MOE_GATE_CHANNEL)
-        Vec8<float>::store(o + 2 * plane, acc_gate[i], H - c);
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      if (grp > 0 && c < H) Vec8<float>::store(join + (grp - 1) * H + c, acc[i], H - c);
     }
-  }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int c = (gt + i * stride) * 8;
+      if (c >= H) continue;
+      float f[8], o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = acc[i][j];
+      for (int q = 0; q < p.groups - 1; ++q) {
+        load_w(join + q * H, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += f[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] *= k;
+      if (w) {
+        load_w(w, c, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= f[j];
+      }
+      Vec8<float>::store(p.part + ((long long)plane * gridDim.x + blockIdx.x) * H + c, o, H - c);
+    }
+  };
+  if (a.dw_pre) finish(acc_pre, 0, nullptr, 1.0f);
+  if (a.dw_post) finish(acc_b, 1, channel ? static_cast<const float*>(a.gate) : nullptr, a.beta);
+  if (a.dgate && channel) finish(acc_b, 2, a.w_post, a.beta);
 }
 
-// out[c] = sum over the slots of part[slot][c], 64 channels a workgroup, four
-// slot quarters side by side, added in order (blockIdx.y picks the plane).
-__global__ __launch_bounds__(256) void channel_sum_kernel(const float* part, int slots, int H,
-                                                           float* o0, float* o1, float* o2) {
-  __shared__ float s[4][64];
+// out[c] = sum over the slots of part[slot][c]: 64 channels a workgroup, its 16
+// waves taking a sixteenth of the slots each, added in wave order (blockIdx.y
+// picks the plane).
+__global__ __launch_bounds__(1024) void channel_sum_kernel(const float* part, int slots, int H,
+                                                            float* o0, float* o1, float* o2) {
+  __shared__ float s[16][64];
   float* out = blockIdx.y == 0 ? o0 : (blockIdx.y == 1 ? o1 : o2);
   if (!out) return;
   const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
@@ -341,28 +392,48 @@ __global__ __launch_bounds__(256) void channel_sum_kernel(const float* part, int
   const float* src = part + (long long)blockIdx.y * slots * H;
   float t = 0.0f;
   if (c < H) {
-    const int lo = (int)((long long)slots * q / 4), hi = (int)((long long)slots * (q + 1) / 4);
+    const int lo = slots * q / 16, hi = slots * (q + 1) / 16;
+#pragma unroll 16
     for (int i = lo; i < hi; ++i) t += src[(long long)i * H + c];
   }
   s[q][lane] = t;
   __syncthreads();
-  if (q == 0 && c < H) out[c] = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+  if (q == 0 && c < H) {
+    t = s[0][lane];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += s[i][lane];
+    out[c] = t;
+  }
 }
 
 int bwd_blocks(int T, int H, int cus) {
-  const RowShape s = row_shape(H);
-  const int need = (T + s.groups - 1) / s.groups;
+  const int groups = row_shape(H, kBwdWaves).groups;
+  const int need = (T + groups - 1) / groups;
   return need < cus ? need : cus;
 }
 
 constexpr int kMaxCus = 256;    // workspace bound: blocks never exceed this
 
-template <typename P>
-using kernel_t = void (*)(P);
+template <typename E>
+struct Type {
+  using type = E;
+};
 
-template <typename P>
-kernel_t<P> pick(kernel_t<P> (&table)[2][2][2], moe_dtype_t x, moe_dtype_t b, int items) {
-  return table[x == MOE_F32][b == MOE_F32][items - 1];
+// f(X, B, items) with the row types and the vectors a thread owns as types
+template <typename F>
+void with_types(moe_dtype_t x, moe_dtype_t b, int items, F f) {
+  auto with_items = [&](auto xt, auto bt) {
+    if (items == 1) f(xt, bt, std::integral_constant<int, 1>{});
+    else if (items == 2) f(xt, bt, std::integral_constant<int, 2>{});
+    else f(xt, bt, std::integral_constant<int, 4>{});
+  };
+  if (x == MOE_BF16) {
+    if (b == MOE_BF16) with_items(Type<bf16_t>{}, Type<bf16_t>{});
+    else with_items(Type<bf16_t>{}, Type<float>{});
+  } else {
+    if (b == MOE_BF16) with_items(Type<float>{}, Type<bf16_t>{});
+    else with_items(Type<float>{}, Type<float>{});
+  }
 }
 
 bool bad_ld(const void* p, long long ld, int H) { return p && ld < H; }
@@ -390,23 +461,22 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_args* args, hipStrea
       !element_aligned(a.gate, a.gate_mode == MOE_GATE_FULL ? a.b_dtype : MOE_F32))
     return MOE_ERR_ALIGN;
   if (moe_status_t s = check_device()) return s;
-  const RowShape s = row_shape(a.H);
+  const RowShape s = row_shape(a.H, kFwdWaves);
   FwdParams p{a, s.wpr, s.groups};
   if (!a.b) p.a.gate_mode = MOE_GATE_NONE;
-  static kernel_t<FwdParams> table[2][2][2] = {
-      {{block_norm_kernel<bf16_t, bf16_t, 1>, block_norm_kernel<bf16_t, bf16_t, 2>},
-       {block_norm_kernel<bf16_t, float, 1>, block_norm_kernel<bf16_t, float, 2>}},
-      {{block_norm_kernel<float, bf16_t, 1>, block_norm_kernel<float, bf16_t, 2>},
-       {block_norm_kernel<float, float, 1>, block_norm_kernel<float, float, 2>}}};
   const int blocks = (a.T + s.groups - 1) / s.groups;
-  hipLaunchKernelGGL(pick(table, a.x_dtype, a.b_dtype, s.items), dim3(blocks),
-                     dim3(s.wpr * s.groups * 64), 0, stream, p);
+  with_types(a.x_dtype, a.b_dtype, s.items, [&](auto x, auto b, auto items) {
+    using X = typename decltype(x)::type;
+    using B = typename decltype(b)::type;
+    hipLaunchKernelGGL((block_norm_kernel<X, B, decltype(items)::value>), dim3(blocks),
+                       dim3(s.wpr * s.groups * 64), 0, stream, p);
+  });
   return launch_status();
 }
 
 extern "C" size_t moe_block_norm_backward_workspace_bytes(int T, int H) {
   if (T <= 0 || H <= 0 || H > kMaxWidth) return 0;
-  return (size_t)bwd_blocks(T, H, kMaxCus) * row_shape(H).groups * 3 * H * sizeof(float);
+  return (size_t)bwd_blocks(T, H, kMaxCus) * 3 * H * sizeof(float);
 }
 
 extern "C" moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* args, void* ws,
@@ -446,26 +516,30 @@ extern "C" moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* a
     return MOE_OK;
   }
   if (moe_status_t s = check_device()) return s;
-  const RowShape s = row_shape(a.H);
+  const RowShape s = row_shape(a.H, kBwdWaves);
   int slots = 0;
   if (a.T > 0) {
     int cus = cu_count();
     if (cus < 1 || cus > kMaxCus) cus = kMaxCus;
-    const int blocks = bwd_blocks(a.T, a.H, cus);
-    slots = blocks * s.groups;
+    slots = bwd_blocks(a.T, a.H, cus);
     BwdParams p{a, s.wpr, s.groups, static_cast<float*>(ws)};
     if (!a.b) p.a.gate_mode = MOE_GATE_NONE;
-    static kernel_t<BwdParams> table[2][2][2] = {
-        {{block_norm_bwd_kernel<bf16_t, bf16_t, 1>, block_norm_bwd_kernel<bf16_t, bf16_t, 2>},
-         {block_norm_bwd_kernel<bf16_t, float, 1>, block_norm_bwd_kernel<bf16_t, float, 2>}},
-        {{block_norm_bwd_kernel<float, bf16_t, 1>, block_norm_bwd_kernel<float, bf16_t, 2>},
-         {block_norm_bwd_kernel<float, float, 1>, block_norm_bwd_kernel<float, float, 2>}}};
-    hipLaunchKernelGGL(pick(table, a.x_dtype, a.b_dtype, s.items), dim3(blocks),
-                       dim3(s.wpr * s.groups * 64), 0, stream, p);
+    const size_t lds = sums ? (size_t)(s.groups - 1) * a.H * sizeof(float) : 0;
+    with_types(a.x_dtype, a.b_dtype, s.items, [&](auto x, auto b, auto items) {
+      using X = typename decltype(x)::type;
+      using B = typename decltype(b)::type;
+      constexpr int ITEMS = decltype(items)::value < 2 ? 1 : 2;      // 16 waves never need 4
+      if (p.a.gate_mode == MOE_GATE_FULL)
+        hipLaunchKernelGGL((block_norm_bwd_kernel<X, B, ITEMS, true>), dim3(slots),
+                           dim3(s.wpr * s.groups * 64), lds, stream, p);
+      else
+        hipLaunchKernelGGL((block_norm_bwd_kernel<X, B, ITEMS, false>), dim3(slots),
+                           dim3(s.wpr * s.groups * 64), lds, stream, p);
+    });
     if (moe_status_t st = launch_status()) return st;
   }
   if (sums)
-    hipLaunchKernelGGL(channel_sum_kernel, dim3((a.H + 63) / 64, 3), dim3(256), 0, stream,
+    hipLaunchKernelGGL(channel_sum_kernel, dim3((a.H + 63) / 64, 3), dim3(1024), 0, stream,
                        static_cast<const float*>(ws), slots, a.H, a.dw_pre, a.dw_post,
                        a.gate_mode == MOE_GATE_CHANNEL ? static_cast<float*>(a.dgate) : nullptr);
   return launch_status();

@@ -4,9 +4,10 @@
 //   norm  = sqrt(sumsq),  coef = min(1, max_norm / (norm + 1e-6)), 1 where the
 //   norm is not finite;  dst = coef * src  (rounded once to dst's type)
 //
-// The tensors are cut into chunks of 16384 elements, numbered through in list
+// The tensors are cut into chunks of 4096 elements, numbered through in list
 // order; a workgroup takes a contiguous range of chunk numbers, so the split
-// is even whatever the tensors' sizes.  Squares are summed in double: no
+// is even whatever the tensors' sizes, and walks its range one stretch (the
+// chunks of one tensor) after the other.  Squares are summed in double: no
 // gradient overflows or vanishes in the sum, and the partial sums are added
 // in a fixed order, so the norm is the same on every run.
 #include <algorithm>
@@ -19,7 +20,7 @@ namespace {
 
 using namespace moe;
 
-constexpr int kChunk = 16384;
+constexpr int kChunk = 4096;
 constexpr int kThreads = 256;
 constexpr int kMaxBlocks = 2048;
 constexpr float kEps = 1e-6f;
@@ -39,29 +40,36 @@ struct ListParams {
   long long chunks;
 };
 
-// the last tensor whose first chunk is <= c (empty tensors own no chunk)
+// The last tensor whose first chunk is <= c (empty tensors own no chunk),
+// searched 64 at a time by the lanes of each wave.
 __device__ __forceinline__ int find_tensor(const ListParams& p, long long c) {
-  int lo = 0, hi = p.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.table[mid].first_chunk <= c) lo = mid;
-    else hi = mid - 1;
+  int lo = 0, n = p.n;                  // it is one of lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int at = (threadIdx.x & 63) * step;
+    const bool before = at < n && p.table[lo + at].first_chunk <= c;
+    const int last = (int)__builtin_popcountll(__ballot(before)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// calls f(entry, first element, elements) for this workgroup's chunks
+// calls f(entry, first element, elements) for the stretches of this
+// workgroup's range
 template <typename F>
-__device__ __forceinline__ void for_chunks(const ListParams& p, F f) {
+__device__ __forceinline__ void for_stretches(const ListParams& p, F f) {
   const long long lo = p.chunks * blockIdx.x / gridDim.x, hi = p.chunks * (blockIdx.x + 1) / gridDim.x;
   if (lo >= hi) return;
-  int t = find_tensor(p, lo);
-  for (long long c = lo; c < hi; ++c) {
-    while (t + 1 < p.n && p.table[t + 1].first_chunk <= c) ++t;
+  long long c = lo;
+  for (int t = find_tensor(p, lo); c < hi; ++t) {
     const Entry e = p.table[t];
+    const long long own = (e.numel + kChunk - 1) / kChunk;
+    const long long end = min(hi, e.first_chunk + own);
+    if (end <= c) continue;
     const long long at = (c - e.first_chunk) * kChunk;
-    const long long left = e.numel - at;
-    f(e, at, (int)(left < kChunk ? left : kChunk));
+    f(e, at, min(e.numel, (end - e.first_chunk) * kChunk) - at);
+    c = end;
   }
 }
 
@@ -76,25 +84,46 @@ __device__ __forceinline__ double block_sum(double v) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-template <typename E>
-__device__ __forceinline__ double chunk_squares(const E* p, int n) {
-  double t = 0.0;
-  for (int c = threadIdx.x * 8; c < n; c += kThreads * 8) {
+// Walks the n elements at p, eight a thread and kUnroll vectors at a time so
+// that their loads are in flight together; g(element index, value vector).
+constexpr int kUnroll = 4;
+template <typename E, typename G>
+__device__ __forceinline__ void walk(const E* p, long long n, G g) {
+  constexpr int kSpan = kThreads * 8;
+  long long c = threadIdx.x * 8;
+  const long long whole = n - (long long)(kUnroll - 1) * kSpan - 8;
+  for (; c <= whole; c += kUnroll * kSpan) {
+    Vec8<E> x[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) x[k].load(p + c + k * kSpan, 8);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) g(c + k * kSpan, x[k], 8);
+  }
+  for (; c < n; c += kSpan) {
+    const int valid = (int)min(n - c, 8LL);
     Vec8<E> x;
-    x.load(p + c, n - c);
+    x.load(p + c, valid);
+    g(c, x, valid);
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ double squares(const E* p, long long n) {
+  double t = 0.0;
+  walk(p, n, [&](long long, const Vec8<E>& x, int) {
     float v[8];
     x.get(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) t = __builtin_fma((double)v[j], (double)v[j], t);
-  }
+  });
   return t;
 }
 
 __global__ __launch_bounds__(kThreads) void square_sum_kernel(ListParams p, double* part) {
   double t = 0.0;
-  for_chunks(p, [&](const Entry& e, long long at, int n) {
-    t += e.src_f32 ? chunk_squares(static_cast<const float*>(e.src) + at, n)
-                   : chunk_squares(static_cast<const bf16_t*>(e.src) + at, n);
+  for_stretches(p, [&](const Entry& e, long long at, long long n) {
+    t += e.src_f32 ? squares(static_cast<const float*>(e.src) + at, n)
+                   : squares(static_cast<const bf16_t*>(e.src) + at, n);
   });
   t = block_sum(t);
   if (threadIdx.x == 0) part[blockIdx.x] = t;
@@ -116,16 +145,14 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const double* part, in
 }
 
 template <typename S, typename D>
-__device__ __forceinline__ void scale_chunk(const S* s, D* d, int n, float coef) {
-  for (int c = threadIdx.x * 8; c < n; c += kThreads * 8) {
-    Vec8<S> x;
-    x.load(s + c, n - c);
+__device__ __forceinline__ void scale(const S* s, D* d, long long n, float coef) {
+  walk(s, n, [&](long long c, const Vec8<S>& x, int valid) {
     float v[8];
     x.get(v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= coef;
-    Vec8<D>::store(d + c, v, n - c);
-  }
+    Vec8<D>::store(d + c, v, valid);
+  });
 }
 
 // Scales every tensor.  `part` holds `parts` partial sums of squares (one:
@@ -140,16 +167,16 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(ListParams p, const dou
     result[0] = norm;
     result[1] = coef;
   }
-  for_chunks(p, [&](const Entry& e, long long at, int n) {
+  for_stretches(p, [&](const Entry& e, long long at, long long n) {
     if (coef == 1.0f && e.src == e.dst) return;      // nothing to change in place
     if (e.src_f32) {
       const float* s = static_cast<const float*>(e.src) + at;
-      if (e.dst_f32) scale_chunk(s, static_cast<float*>(e.dst) + at, n, coef);
-      else scale_chunk(s, static_cast<bf16_t*>(e.dst) + at, n, coef);
+      if (e.dst_f32) scale(s, static_cast<float*>(e.dst) + at, n, coef);
+      else scale(s, static_cast<bf16_t*>(e.dst) + at, n, coef);
     } else {
       const bf16_t* s = static_cast<const bf16_t*>(e.src) + at;
-      if (e.dst_f32) scale_chunk(s, static_cast<float*>(e.dst) + at, n, coef);
-      else scale_chunk(s, static_cast<bf16_t*>(e.dst) + at, n, coef);
+      if (e.dst_f32) scale(s, static_cast<float*>(e.dst) + at, n, coef);
+      else scale(s, static_cast<bf16_t*>(e.dst) + at, n, coef);
     }
   });
 }
