@@ -54,12 +54,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[kMaxWaves],
     for (int i = 0; i < N; ++i) red[i][wave] = v[i];
   }
   __syncthreads();
+  const int w = lane & 15;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float t = 0.0f;
-    for (int w = 0; w < wpr; ++w) t += red[i][first_wave + w];
-    v[i] = t;
-  }
+  for (int i = 0; i < N; ++i) v[i] = row16_sum(w < wpr ? red[i][first_wave + w] : 0.0f);
 }
 
 struct FwdParams {
