@@ -26,9 +26,10 @@
 //     so that ds_read_b128 has no bank conflicts.  Crossed half tile: [64 k]
 //     [128 columns], swizzled for ds_read_b64_tr_b16, which hands each lane
 //     four k values of its column.
-//   * Row tiles of a group are of equal height (a multiple of 16 rows), and a
-//     tile of fewer than 256 rows skips the MFMAs of its empty subtiles (the
-//     loop is compiled for each count).
+//   * A tile of fewer than 256 rows skips the MFMAs of its empty subtiles (the
+//     loop is compiled for each count); one of at most 128 rows has no second
+//     half of A, and runs two phases a step over three steps in LDS
+//     (ShortProduct).
 //   * Rows past a group's end, columns past the matrix and the tail of k are
 //     given offsets beyond the buffer resource's size and read as zero, so
 //     they never meet the group's data, whatever they hold.
@@ -52,7 +53,7 @@ constexpr int kThreads = 512;
 constexpr int kTile = 256;                 // rows and columns of a tile
 constexpr int kStep = 64;                  // contraction depth of a step
 constexpr int kHalf = 128 * kStep * 2;     // bytes of a half tile
-constexpr int kLds = 8 * kHalf;            // [A, B][half][step parity]
+constexpr int kLds = 9 * kHalf;            // [A, B][half][step parity], or 3 x [A, B0, B1]
 constexpr uint32_t kOut = 0x80000000u;     // an offset past every buffer (all are below 2^31)
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
@@ -92,20 +93,15 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// The K loop.  A_X / B_X: crossed operand; A_G / B_G: gathered crossed operand;
-// L0, L1: 16-row subtiles per wave with rows in A's first and second half.
-template <bool A_X, bool B_X, bool A_G, bool B_G, int L0, int L1>
-struct Product {
-  static constexpr int kIdx = 2 * (A_G ? 1 : 0) + 2 * (B_G ? 1 : 0);   // index loads a step
+// Copies and fragment reads.  A_X / B_X: crossed operand.
+template <bool A_X, bool B_X>
+struct Tile {
   f32x4 acc[2][4][2][2];        // [A half][subtile][B half][subtile]
-  bf16x8 a0[4][2], a1[4][2], b0[2][2], b1[2][2];
-  int ia[2][2], ib[2][2];       // gathered rows of the two steps ahead, [step parity][j]
-
   uint8_t* smem;
   int wave, lane, n_steps;
   const Operand &A, &B;
 
-  __device__ __forceinline__ Product(uint8_t* s, int w, int l, int n, const Operand& a, const Operand& b)
+  __device__ __forceinline__ Tile(uint8_t* s, int w, int l, int n, const Operand& a, const Operand& b)
       : smem(s), wave(w), lane(l), n_steps(n), A(a), B(b) {}
 
   template <bool X, bool G>
@@ -146,9 +142,6 @@ struct Product {
     for (int j = 0; j < 2; ++j) idx[j] = o.index[min(first + 32 * j, o.rows - 1)];
   }
 
-  __device__ __forceinline__ uint8_t* slot(int op, int h, int par) {
-    return smem + ((op * 2 + h) * 2 + par) * kHalf;
-  }
   // MFMA fragment of 16 rows (columns) and 32 k values
   __device__ __forceinline__ bf16x8 crossed(const uint8_t* s, int blk, int kk) {
     const int lk = lane >> 4, a = (lane & 15) >> 2, q = lane & 3;
@@ -195,93 +188,113 @@ struct Product {
     __builtin_amdgcn_s_setprio(0);
   }
 
+  template <int H, int L>
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) acc[H][i][u][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+};
+
+// The K loop.  A_G / B_G: gathered crossed operand; L0, L1: 16-row subtiles per
+// wave with rows in A's first and second half.
+template <bool A_X, bool B_X, bool A_G, bool B_G, int L0, int L1>
+struct Product : Tile<A_X, B_X> {
+  using T = Tile<A_X, B_X>;
+  using T::A, T::B, T::smem, T::wave, T::n_steps;
+  static constexpr int kIdx = 2 * (A_G ? 1 : 0) + 2 * (B_G ? 1 : 0);   // index loads a step
+  bf16x8 a0[4][2], a1[4][2], b0[2][2], b1[2][2];
+  int ia[2][2], ib[2][2];       // gathered rows of the two steps ahead, [step parity][j]
+  using T::T;
+
+  __device__ __forceinline__ uint8_t* slot(int op, int h, int par) {
+    return smem + ((op * 2 + h) * 2 + par) * kHalf;
+  }
+
   // One step in four phases.  PAR: parity of the step's slots.
   template <int PAR>
   __device__ __forceinline__ void step(int s) {
     // phase 0: rest of A0 and all of B0; quadrant (A0, B0)
     if constexpr (L0 > 3) {
-      a0[3][0] = read_a(slot(0, 0, PAR), 3, 0);
-      a0[3][1] = read_a(slot(0, 0, PAR), 3, 1);
+      a0[3][0] = this->read_a(slot(0, 0, PAR), 3, 0);
+      a0[3][1] = this->read_a(slot(0, 0, PAR), 3, 1);
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) b0[t][kk] = read_b(slot(1, 0, PAR), t, kk);
-    copy<A_X, A_G>(A, slot(0, 1, PAR ^ 1), 1, s + 1, ia[PAR ^ 1]);
+      for (int kk = 0; kk < 2; ++kk) b0[t][kk] = this->read_b(slot(1, 0, PAR), t, kk);
+    this->template copy<A_X, A_G>(A, slot(0, 1, PAR ^ 1), 1, s + 1, ia[PAR ^ 1]);
     wait_vm<6 + kIdx>();
     barrier();
-    quadrant<0, L0>(a0, b0, 0);
+    this->template quadrant<0, L0>(a0, b0, 0);
     barrier();
     // phase 1: B1, first of A1; quadrant (A0, B1)
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) b1[t][kk] = read_b(slot(1, 1, PAR), t, kk);
+      for (int kk = 0; kk < 2; ++kk) b1[t][kk] = this->read_b(slot(1, 1, PAR), t, kk);
     if constexpr (L1 > 0) {
-      a1[0][0] = read_a(slot(0, 1, PAR), 0, 0);
-      a1[0][1] = read_a(slot(0, 1, PAR), 0, 1);
+      a1[0][0] = this->read_a(slot(0, 1, PAR), 0, 0);
+      a1[0][1] = this->read_a(slot(0, 1, PAR), 0, 1);
     }
-    copy<B_X, B_G>(B, slot(1, 1, PAR ^ 1), 1, s + 1, ib[PAR ^ 1]);
+    this->template copy<B_X, B_G>(B, slot(1, 1, PAR ^ 1), 1, s + 1, ib[PAR ^ 1]);
     barrier();
-    quadrant<0, L0>(a0, b1, 1);
+    this->template quadrant<0, L0>(a0, b1, 1);
     barrier();
     // phase 2: rest of A1; quadrant (A1, B1)
 #pragma unroll
     for (int i = 1; i < L1; ++i) {
-      a1[i][0] = read_a(slot(0, 1, PAR), i, 0);
-      a1[i][1] = read_a(slot(0, 1, PAR), i, 1);
+      a1[i][0] = this->read_a(slot(0, 1, PAR), i, 0);
+      a1[i][1] = this->read_a(slot(0, 1, PAR), i, 1);
     }
-    copy<A_X, A_G>(A, slot(0, 0, PAR), 0, s + 2, ia[PAR]);
+    this->template copy<A_X, A_G>(A, slot(0, 0, PAR), 0, s + 2, ia[PAR]);
     wait_vm<8 + kIdx>();
     barrier();
-    quadrant<1, L1>(a1, b1, 1);
+    this->template quadrant<1, L1>(a1, b1, 1);
     barrier();
     // phase 3: most of the next step's A0; quadrant (A1, B0)
 #pragma unroll
     for (int i = 0; i < (L0 < 3 ? L0 : 3); ++i) {
-      a0[i][0] = read_a(slot(0, 0, PAR ^ 1), i, 0);
-      a0[i][1] = read_a(slot(0, 0, PAR ^ 1), i, 1);
+      a0[i][0] = this->read_a(slot(0, 0, PAR ^ 1), i, 0);
+      a0[i][1] = this->read_a(slot(0, 0, PAR ^ 1), i, 1);
     }
-    if constexpr (A_G) load_index(A, s + 3, ia[PAR ^ 1]);
-    if constexpr (B_G) load_index(B, s + 3, ib[PAR ^ 1]);
+    if constexpr (A_G) this->load_index(A, s + 3, ia[PAR ^ 1]);
+    if constexpr (B_G) this->load_index(B, s + 3, ib[PAR ^ 1]);
     __builtin_amdgcn_sched_barrier(0);
-    copy<B_X, B_G>(B, slot(1, 0, PAR), 0, s + 2, ib[PAR]);
+    this->template copy<B_X, B_G>(B, slot(1, 0, PAR), 0, s + 2, ib[PAR]);
     wait_vm<8 + kIdx>();
     barrier();
-    quadrant<1, L1>(a1, b0, 0);
+    this->template quadrant<1, L1>(a1, b0, 0);
     barrier();
   }
 
   __device__ __forceinline__ void run() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) acc[h][i][u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    this->template clear<0, L0>();
+    this->template clear<1, L1>();
     if (n_steps == 0) return;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      if constexpr (A_G) load_index(A, s, ia[s]);
-      if constexpr (B_G) load_index(B, s, ib[s]);
+      if constexpr (A_G) this->load_index(A, s, ia[s]);
+      if constexpr (B_G) this->load_index(B, s, ib[s]);
     }
-    copy<A_X, A_G>(A, slot(0, 0, 0), 0, 0, ia[0]);
-    copy<B_X, B_G>(B, slot(1, 0, 0), 0, 0, ib[0]);
-    copy<A_X, A_G>(A, slot(0, 1, 0), 1, 0, ia[0]);
-    copy<B_X, B_G>(B, slot(1, 1, 0), 1, 0, ib[0]);
-    if constexpr (A_G) load_index(A, 2, ia[0]);
-    if constexpr (B_G) load_index(B, 2, ib[0]);
+    this->template copy<A_X, A_G>(A, slot(0, 0, 0), 0, 0, ia[0]);
+    this->template copy<B_X, B_G>(B, slot(1, 0, 0), 0, 0, ib[0]);
+    this->template copy<A_X, A_G>(A, slot(0, 1, 0), 1, 0, ia[0]);
+    this->template copy<B_X, B_G>(B, slot(1, 1, 0), 1, 0, ib[0]);
+    if constexpr (A_G) this->load_index(A, 2, ia[0]);
+    if constexpr (B_G) this->load_index(B, 2, ib[0]);
     __builtin_amdgcn_sched_barrier(0);
-    copy<A_X, A_G>(A, slot(0, 0, 1), 0, 1, ia[1]);
-    copy<B_X, B_G>(B, slot(1, 0, 1), 0, 1, ib[1]);
+    this->template copy<A_X, A_G>(A, slot(0, 0, 1), 0, 1, ia[1]);
+    this->template copy<B_X, B_G>(B, slot(1, 0, 1), 0, 1, ib[1]);
     wait_vm<8>();            // A0 and B0 of step 0
     barrier();
 #pragma unroll
     for (int i = 0; i < (L0 < 3 ? L0 : 3); ++i) {
-      a0[i][0] = read_a(slot(0, 0, 0), i, 0);
-      a0[i][1] = read_a(slot(0, 0, 0), i, 1);
+      a0[i][0] = this->read_a(slot(0, 0, 0), i, 0);
+      a0[i][1] = this->read_a(slot(0, 0, 0), i, 1);
     }
     if (wave >= 4) barrier();     // half a phase behind
     int s = 0;
@@ -292,6 +305,84 @@ struct Product {
     if (s < n_steps) step<0>(s);
     if (wave < 4) barrier();
     wait_vm<0>();            // copies in flight would land in the next user's LDS
+  }
+};
+
+// The K loop of a tile of at most 128 rows (straight A): two phases a step,
+// [A, B0, B1] of three steps in LDS, each requested two steps ahead into
+// the slots that were last read two phases ago.  L: 16-row subtiles per wave.
+template <bool B_X, int L>
+struct ShortProduct : Tile<false, B_X> {
+  using T = Tile<false, B_X>;
+  using T::A, T::B, T::smem, T::wave, T::n_steps;
+  static constexpr int kAhead = L < 2 ? L : 2;     // subtiles of A read a phase early
+  bf16x8 a0[4][2], b0[2][2], b1[2][2];
+  int none[2];
+  using T::T;
+
+  __device__ __forceinline__ uint8_t* slot(int which, int stage) { return smem + (stage * 3 + which) * kHalf; }
+  __device__ __forceinline__ void read_a_part(int stage, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < lo || i >= hi) continue;
+      a0[i][0] = this->read_a(slot(0, stage), i, 0);
+      a0[i][1] = this->read_a(slot(0, stage), i, 1);
+    }
+  }
+
+  // STAGE: the step's slots.
+  template <int STAGE>
+  __device__ __forceinline__ void step(int s) {
+    constexpr int kNext = (STAGE + 1) % 3, kRefill = (STAGE + 2) % 3;
+    // phase 0: rest of A and all of B0; quadrant (A, B0)
+    read_a_part(STAGE, kAhead, L);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) b0[t][kk] = this->read_b(slot(1, STAGE), t, kk);
+    this->template copy<false, false>(A, slot(0, kRefill), 0, s + 2, none);
+    this->template copy<B_X, false>(B, slot(1, kRefill), 0, s + 2, none);
+    wait_vm<8>();
+    barrier();
+    this->template quadrant<0, L>(a0, b0, 0);
+    barrier();
+    // phase 1: B1; quadrant (A, B1).  The next step's first subtiles of A are
+    // read into their registers behind the MFMAs.
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) b1[t][kk] = this->read_b(slot(2, STAGE), t, kk);
+    this->template copy<B_X, false>(B, slot(2, kRefill), 1, s + 2, none);
+    wait_vm<8>();
+    barrier();
+    this->template quadrant<0, L>(a0, b1, 1);
+    read_a_part(kNext, 0, kAhead);
+    barrier();
+  }
+
+  __device__ __forceinline__ void run() {
+    this->template clear<0, L>();
+    if (n_steps == 0) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      this->template copy<false, false>(A, slot(0, s), 0, s, none);
+      this->template copy<B_X, false>(B, slot(1, s), 0, s, none);
+      this->template copy<B_X, false>(B, slot(2, s), 1, s, none);
+    }
+    wait_vm<8>();            // A and B0 of step 0
+    barrier();
+    read_a_part(0, 0, kAhead);
+    if (wave >= 4) barrier();     // half a phase behind
+    int s = 0;
+    for (; s + 3 <= n_steps; s += 3) {
+      step<0>(s);
+      step<1>(s + 1);
+      step<2>(s + 2);
+    }
+    if (s < n_steps) step<0>(s);
+    if (s + 1 < n_steps) step<1>(s + 1);
+    if (wave < 4) barrier();
+    wait_vm<0>();
   }
 };
 
@@ -322,72 +413,19 @@ __device__ __forceinline__ void crossed_offsets(Operand& o, int wave, int lane, 
                         : (gathered ? 0u : (uint32_t)(k + 32 * j) * ld2) + h * 256 + chunk * 16;
 }
 
-// ---- the tile list of the forward product and the input gradient.  Groups
-// are taken from the last to the first (the shared expert, whose tiles are
-// all full, starts first), each as bands of up to kBand row tiles, column tile by
-// column tile.  32 consecutive tiles, one round of an XCD's compute units,
-// go to one XCD: they share a few row and column tiles through its L2.
-constexpr int kBand = 4;
+// ---- forward product and input gradient.
 
+// A tile: rows m0 .. m0 + m_rows - 1 of group g (which starts at row row0),
+// columns n0 .. n0 + cols - 1.
 struct TileAt {
-  int g, row0, rows, m0, m_rows, n_tile;
+  int g, row0, m0, m_rows, n0, cols;
 };
-
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int G, int total, int n_tiles,
-                                          int* tmp, TileAt& t) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
-  const int want = (slot >> 5) * 256 + xcd * 32 + (slot & 31);
-  int done = 0;                       // row tiles x column tiles of the groups so far
-  for (int base = 0; base < G; base += kThreads) {
-    const int gi = G - 1 - (base + tid);
-    int lo = 0, n = 0;
-    if (gi >= 0) {
-      lo = clampi(offsets[gi], 0, total);
-      n = max(clampi(offsets[gi + 1], 0, total) - lo, 0);
-    }
-    const int mt = (n + kTile - 1) / kTile, own = mt * n_tiles;
-    int incl = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 63) tmp[wave] = incl;
-    __syncthreads();
-    int before = done + incl - own;
-#pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) {
-      if (w < wave) before += tmp[w];
-      done += tmp[w];
-    }
-    if (want >= before && want < before + own) {
-      const int local = want - before;
-      const int band = local / (kBand * n_tiles), in = local - band * kBand * n_tiles;
-      const int height = min(kBand, mt - band * kBand);
-      const int n_tile = in / height, m = band * kBand + in - n_tile * height;
-      const int per = ((n + 15) / 16 + mt - 1) / mt * 16;      // rows of a tile
-      tmp[8] = gi, tmp[9] = lo, tmp[10] = n, tmp[11] = m * per, tmp[12] = n_tile, tmp[13] = per;
-    }
-    __syncthreads();
-    if (want < done) {
-      t.g = __builtin_amdgcn_readfirstlane(tmp[8]);
-      t.row0 = __builtin_amdgcn_readfirstlane(tmp[9]);
-      t.rows = __builtin_amdgcn_readfirstlane(tmp[10]);
-      t.m0 = __builtin_amdgcn_readfirstlane(tmp[11]);
-      t.n_tile = __builtin_amdgcn_readfirstlane(tmp[12]);
-      t.m_rows = min(__builtin_amdgcn_readfirstlane(tmp[13]), t.rows - t.m0);
-      return t.m_rows > 0;
-    }
-  }
-  return false;
-}
 
 template <bool KN, int L0, int L1>
 __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const TileAt& t, uint8_t* smem) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int K = a.k_dim, N = a.n_out, n0 = t.n_tile * kTile;
+  const int K = a.k_dim, N = a.n_out;
   Operand A, B;
   {
     // straight A: load j of wave w fills rows 8 (w + 8 j) .. + 7 of a half tile
@@ -399,7 +437,8 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
       for (int j = 0; j < 2; ++j) {
         const int r = h * 128 + 8 * (wave + 8 * j) + (lane >> 3);
         rows[h][j] = -1;
-        if (r < t.m_rows) rows[h][j] = a.a_row_index ? clampi(a.a_row_index[t.row0 + t.m0 + r], 0, a.a_rows - 1) : r;
+        if (r < t.m_rows && (h == 0 || L1 > 0))
+          rows[h][j] = a.a_row_index ? clampi(a.a_row_index[t.row0 + t.m0 + r], 0, a.a_rows - 1) : r;
       }
     const uint8_t* base = static_cast<const uint8_t*>(a.a);
     A.base = a.a_row_index ? base : base + (long long)(t.row0 + t.m0) * a.lda * 2;
@@ -408,10 +447,10 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
   }
   const uint8_t* b = static_cast<const uint8_t*>(a.b) + (long long)t.g * N * K * 2;
   if constexpr (KN) {
-    B.base = b + (long long)n0 * 2;
+    B.base = b + (long long)t.n0 * 2;
     B.index = nullptr;
     B.rows = K;
-    crossed_offsets(B, wave, lane, (uint32_t)N * 2, N - n0, false);
+    crossed_offsets(B, wave, lane, (uint32_t)N * 2, t.cols, false);
   } else {
     const int chunk = (lane & 7) ^ (((lane >> 4) & 1) | ((wave & 3) << 1));
     long long rows[2][2];
@@ -420,13 +459,14 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = h * 128 + 8 * (wave + 8 * j) + (lane >> 3);
-        rows[h][j] = n0 + r < N ? r : -1;
+        rows[h][j] = r < t.cols ? r : -1;
       }
-    B.base = b + (long long)n0 * K * 2;
-    B.bytes = (uint32_t)min(kTile, N - n0) * (uint32_t)K * 2;
+    B.base = b + (long long)t.n0 * K * 2;
+    B.bytes = (uint32_t)t.cols * (uint32_t)K * 2;
     straight_offsets(B, rows, K, chunk, K);
   }
-  Product<false, KN, false, false, L0, L1> p(smem, wave, lane, (K + kStep - 1) / kStep, A, B);
+  typename std::conditional<(L1 > 0), Product<false, KN, false, false, L0, L1>,
+                            ShortProduct<KN, L0>>::type p(smem, wave, lane, (K + kStep - 1) / kStep, A, B);
   p.run();
 
   // A lane holds 4 consecutive columns of one row in each accumulator; with a
@@ -444,35 +484,198 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const int c = n0 + u * 128 + wn * 32 + (KN ? v * 16 + lk * 4 : lk * 8 + v * 4);
-          if (c >= N) continue;
+          const int c = u * 128 + wn * 32 + (KN ? v * 16 + lk * 4 : lk * 8 + v * 4);
+          if (c >= t.cols) continue;
+          const long long at = row * a.ldo + t.n0 + c;
           const f32x4 x = p.acc[h][i][u][v] * s;
           if (a.out_dtype == MOE_F32) {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + row * a.ldo + c) = x;
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = x;
           } else {
             bf16x4 y;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
-            *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + row * a.ldo + c) = y;
+            *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at) = y;
           }
         }
     }
 }
 
 template <bool KN>
+__device__ __forceinline__ void short_tile(const moe_gemm_bf16_args& a, const TileAt& t, uint8_t* smem) {
+  const int l0 = (t.m_rows + 31) / 32;
+  if (l0 > 2) l0 > 3 ? gemm_tile<KN, 4, 0>(a, t, smem) : gemm_tile<KN, 3, 0>(a, t, smem);
+  else l0 > 1 ? gemm_tile<KN, 2, 0>(a, t, smem) : gemm_tile<KN, 1, 0>(a, t, smem);
+}
+
+// Rows of group gi (0 for a group past the last).
+__device__ __forceinline__ int group_rows(const int32_t* offsets, int gi, int G, int total, int& lo) {
+  lo = 0;
+  if (gi < 0 || gi >= G) return 0;
+  lo = clampi(offsets[gi], 0, total);
+  return max(clampi(offsets[gi + 1], 0, total) - lo, 0);
+}
+
+// Exclusive prefix of v over the workgroup's threads, and the total.
+__device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int n = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 63) tmp[wave] = incl;
+  __syncthreads();
+  int before = incl - v;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    const int n = tmp[w];
+    if (w < wave) before += n;
+    total += n;
+  }
+  __syncthreads();
+  return before;
+}
+
+// The tile list of the large-batch kernel.  A group's rows are cut into tiles of
+// 256 and a rest, in bands of up to kBand row tiles, column tile by column
+// tile, so that tiles which share a weight tile follow one another.  32
+// consecutive tiles, one round of an XCD's compute units, form a run and go to
+// one XCD: they share a few row and column tiles through its L2.  Runs are
+// dispatched in the order of a golden-ratio stride over the list, not in list
+// order: a group with many rows needs the matrix cores and hardly any
+// memory, one with few rows the reverse, and this way every moment has some
+// of both (in list order the groups' weights arrive at the memory's rate while
+// the matrix cores wait).
+constexpr int kBand = 4;
+constexpr int kRun = 32;
+constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;      // groups of a thread
+
+__device__ __forceinline__ bool find_tile(const moe_gemm_bf16_args& a, int* tmp, TileAt& t) {
+  const int G = a.num_groups, n_tiles = (a.n_out + kTile - 1) / kTile;
+  int lo[kPer], n[kPer], sum = 0, all;
+  const int per = (G + kThreads - 1) / kThreads;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    n[i] = i < per ? group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo[i]) : 0;
+    sum += (n[i] + kTile - 1) / kTile;
+  }
+  int at = prefix(sum, tmp, all) * n_tiles;
+  // the workgroup's place: run j of the dispatch order, tile `in` of it
+  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
+  const int runs = (all * n_tiles + kRun - 1) / kRun;
+  const int j = slot / kRun * 8 + xcd;
+  if (j >= runs) return false;
+  int stride = max((int)(0.618034f * runs), 1);
+  for (;; ++stride) {               // the next one that has no factor in common with the runs
+    int x = runs, y = stride;
+    while (y) {
+      const int r = x % y;
+      x = y;
+      y = r;
+    }
+    if (x == 1) break;
+  }
+  const int want = (int)((long long)j * stride % runs) * kRun + slot % kRun;
+  if (want >= all * n_tiles) return false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int mt = (n[i] + kTile - 1) / kTile;
+    const int in = want - at;
+    if (in >= 0 && in < mt * n_tiles) {
+      const int band = in / (kBand * n_tiles), rest = in - band * kBand * n_tiles;
+      const int height = min(kBand, mt - band * kBand);
+      const int n_tile = rest / height;
+      const int m = band * kBand + rest - n_tile * height;
+      tmp[8] = (int)threadIdx.x * per + i, tmp[9] = lo[i], tmp[10] = m * kTile, tmp[11] = n[i] - m * kTile;
+      tmp[12] = n_tile;
+    }
+    at += mt * n_tiles;
+  }
+  __syncthreads();
+  t.g = __builtin_amdgcn_readfirstlane(tmp[8]);
+  t.row0 = __builtin_amdgcn_readfirstlane(tmp[9]);
+  t.m0 = __builtin_amdgcn_readfirstlane(tmp[10]);
+  t.m_rows = min(__builtin_amdgcn_readfirstlane(tmp[11]), kTile);
+  t.n0 = __builtin_amdgcn_readfirstlane(tmp[12]) * kTile;
+  t.cols = min(kTile, a.n_out - t.n0);
+  return true;
+}
+
+template <bool KN>
 __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(moe_gemm_bf16_args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   TileAt t;
-  if (!find_tile(a.group_offsets, a.num_groups, a.total_rows, (a.n_out + kTile - 1) / kTile,
-                 reinterpret_cast<int*>(smem), t))
-    return;
+  if (!find_tile(a, reinterpret_cast<int*>(smem), t)) return;
   __syncthreads();        // the list's scratch becomes the first half tile
-  const int subtiles = (t.m_rows + 15) / 16;
-  const int l0 = min((subtiles + 1) / 2, 4), l1 = max((subtiles - 8 + 1) / 2, 0);
-  if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(a, t, smem) : gemm_tile<KN, 4, 3>(a, t, smem);
-  else if (l1 > 0) l1 > 1 ? gemm_tile<KN, 4, 2>(a, t, smem) : gemm_tile<KN, 4, 1>(a, t, smem);
-  else if (l0 > 2) l0 > 3 ? gemm_tile<KN, 4, 0>(a, t, smem) : gemm_tile<KN, 3, 0>(a, t, smem);
-  else l0 > 1 ? gemm_tile<KN, 2, 0>(a, t, smem) : gemm_tile<KN, 1, 0>(a, t, smem);
+  const int l1 = (t.m_rows - 128 + 31) / 32;
+  if (t.m_rows <= 128) short_tile<KN>(a, t, smem);
+  else if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(a, t, smem) : gemm_tile<KN, 4, 3>(a, t, smem);
+  else l1 > 1 ? gemm_tile<KN, 4, 2>(a, t, smem) : gemm_tile<KN, 4, 1>(a, t, smem);
+}
+
+// Small groups: the time is the weights' stream, so every workgroup (one per
+// compute unit) streams the same number of weight columns.  Each group with
+// rows counts its columns once per 128 rows, in units of 16, or 64 (a cache
+// line) where a weight row is cut at a unit's edge; workgroup b takes units
+// [U b / blocks, U (b + 1) / blocks), in pieces of at most 256 columns and
+// about equal width inside one group.
+
+template <bool KN>
+__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(moe_gemm_bf16_args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* tmp = reinterpret_cast<int*>(smem);
+  constexpr int kUnit = KN ? 64 : 16;
+  const int G = a.num_groups, units = (a.n_out + kUnit - 1) / kUnit;
+  const int per = (G + kThreads - 1) / kThreads;
+  int sum = 0, lo;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i < per) sum += (group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo) + 127) / 128;
+  int all;
+  const int at = prefix(sum, tmp, all);
+  // row tiles in 64 bits: units of the whole list pass 2^31
+  const long long first = (long long)all * units * blockIdx.x / gridDim.x;
+  const long long last = (long long)all * units * (blockIdx.x + 1) / gridDim.x;
+  if (first >= last) return;
+  const int want = (int)(first / units);      // the row tile that the range starts in
+  int u = (int)(first - (long long)want * units);
+  if (want >= at && want < at + sum) {
+    int m = want - at;
+    for (int i = 0; i < per; ++i) {
+      const int g = (int)threadIdx.x * per + i;
+      const int tiles = (group_rows(a.group_offsets, g, G, a.total_rows, lo) + 127) / 128;
+      if (m < tiles) {
+        tmp[8] = g, tmp[9] = m;
+        break;
+      }
+      m -= tiles;
+    }
+  }
+  __syncthreads();
+  int g = __builtin_amdgcn_readfirstlane(tmp[8]), m = __builtin_amdgcn_readfirstlane(tmp[9]);
+  for (long long left = last - first; left > 0;) {
+    TileAt t;
+    const int rows = group_rows(a.group_offsets, g, G, a.total_rows, t.row0);
+    if (m * 128 >= rows) {        // the group is done, or has no rows
+      ++g, m = 0;
+      continue;
+    }
+    t.g = g;
+    t.m0 = m * 128;
+    t.m_rows = min(rows - t.m0, 128);
+    const int here = (int)min((long long)(units - u), left);      // units of this row tile
+    const int pieces = (here + kTile / kUnit - 1) / (kTile / kUnit);
+    const int take = (here + pieces - 1) / pieces;
+    t.n0 = u * kUnit;
+    t.cols = min(take * kUnit, a.n_out - t.n0);
+    __syncthreads();              // LDS is free again
+    short_tile<KN>(a, t, smem);
+    left -= take;
+    u += take;
+    if (u >= units) u = 0, ++m;
+  }
 }
 
 // ---- weight gradient: one workgroup per 256 x 256 tile of one group's dW.
@@ -561,16 +764,27 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hi
   if (a.a_rows == 0) return MOE_ERR_SHAPE;
   if (!a.group_offsets || !a.out || (a.k_dim > 0 && (!a.a || !a.b))) return MOE_ERR_NULL;
   if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.out)) return MOE_ERR_ALIGN;
-  const long long tiles = ((long long)a.total_rows / kTile +
-                           (a.num_groups < a.total_rows ? a.num_groups : a.total_rows)) *
-                          ((a.n_out + kTile - 1) / kTile);
-  const long long grid = (tiles + 255) / 256 * 256;
-  if (grid > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
   if (moe_status_t s = check_device()) return s;
   const bool kn = a.b_layout == MOE_B_KN;
-  auto kernel = kn ? grouped_gemm_bf16_kernel<true> : grouped_gemm_bf16_kernel<false>;
-  static std::atomic<uint64_t> lds_set[2] = {};
-  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set[kn])) return st;
+  const bool stream_weights = a.total_rows <= 64LL * a.num_groups;
+  long long grid;
+  if (stream_weights) {
+    grid = cu_count();
+    if (grid < 1) grid = 256;
+  } else {
+    const long long tiles = ((long long)a.total_rows / kTile +
+                             (a.num_groups < a.total_rows ? a.num_groups : a.total_rows)) *
+                            ((a.n_out + kTile - 1) / kTile);
+    grid = (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun);
+    if (grid > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
+  }
+  static void (*const table[2][2])(moe_gemm_bf16_args) = {
+      {grouped_gemm_bf16_kernel<false>, grouped_gemm_bf16_kernel<true>},
+      {grouped_gemm_bf16_stream_kernel<false>, grouped_gemm_bf16_stream_kernel<true>}};
+  static std::atomic<uint64_t> lds_set[2][2] = {};
+  const auto kernel = table[stream_weights][kn];
+  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set[stream_weights][kn]))
+    return st;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), kLds, stream, a);
   return launch_status();
 }

@@ -219,7 +219,9 @@ def test_block_norm_no_tokens(moe):
 # grouped products
 
 SIZES = {"ragged": [17, 0, 260, 128, 1], "one": [1], "empty ends": [0, 0, 40, 0],
-         "single": [333], "many": [3] * 70, "large": [0, 700, 300, 515]}
+         "single": [333], "many": [3] * 70, "large": [0, 700, 300, 515],
+         "small with a long one": [5] * 11 + [0] * 20 + [300] + [33, 64, 97, 128, 2] + [0] * 5,
+         "rests": [256, 257, 384, 385, 512, 129, 128, 0, 1000]}
 GEMM_CASES = [
     # sizes, n_out, k, kn, gather, scale, out
     ("ragged", 512, 384, False, True, True, "bf16"),
@@ -236,6 +238,12 @@ GEMM_CASES = [
     ("large", 1288, 1096, False, True, True, "bf16"),
     ("large", 1096, 1288, True, True, True, "bf16"),
     ("large", 512, 128, False, False, False, "bf16"),
+    ("small with a long one", 1288, 200, False, True, True, "bf16"),
+    ("small with a long one", 264, 1032, True, False, False, "f32"),
+    ("small with a long one", 24, 64, True, True, False, "bf16"),
+    ("rests", 520, 456, False, True, False, "bf16"),
+    ("rests", 776, 136, True, False, True, "f32"),
+    ("rests", 256, 8, False, False, False, "f32"),
 ]
 
 
@@ -297,6 +305,8 @@ WGRAD_CASES = [
     ("many", 256, 136, False, True, "bf16", True),
     ("large", 1288, 1096, False, True, "f32", False),
     ("large", 512, 264, False, False, "f32", True),
+    ("rests", 520, 264, True, True, "f32", False),
+    ("small with a long one", 136, 520, True, False, "bf16", False),
 ]
 
 
