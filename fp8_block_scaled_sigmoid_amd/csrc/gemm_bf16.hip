@@ -42,6 +42,7 @@ namespace {
 using namespace moe;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -679,23 +680,106 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(m
 }
 
 // ---- weight gradient: one workgroup per 256 x 256 tile of one group's dW.
+//
+// Most groups have a few hundred rows, so a tile is a few steps and then 256 KB
+// of float results, whose way to memory bounds it.  What that asks for:
+//   * results go through LDS and leave as whole rows of the tile, with
+//     non-temporal stores that do not push the operands out of L2 (straight from
+//     the accumulators, in 64-byte pieces, stores reach 3.8 TB/s; whole cache
+//     lines 5.5, whole rows 5.8);
+//   * an XCD takes an eighth of a group's tiles, column tiles in bands of
+//     kWBand, so that its L2 fetches an eighth of B and A once a band; the
+//     eighths rotate with the group, for groups with fewer than 8 tiles; groups
+//     go from the last (the shared expert, whose tiles are the longest) to the
+//     first.
+// Where there are few tiles, each group's rows are cut into `splits` parts,
+// whose partial sums (float, in the workspace) a second kernel adds in order.
+constexpr int kXcds = 8;
+constexpr int kWBand = 4;
+constexpr int kOutStride = kTile * 4 + 16;      // bytes between rows staged in LDS, off the banks' period
+static_assert(128 * kOutStride <= kLds, "half a tile of float rows fits");
+
+struct WgradParams {
+  moe_wgrad_bf16_args a;
+  int splits;
+  float* part;             // [splits][G][n][k] when splits > 1
+};
+
+// One row piece of 16 bytes, `old` being what accumulation adds to.
+__device__ __forceinline__ void put16(float* o, const uint8_t* s, bool accumulate) {
+  f32x4 x = *reinterpret_cast<const f32x4*>(s);
+  if (accumulate) x += *reinterpret_cast<const f32x4*>(o);
+  __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(o));
+}
+__device__ __forceinline__ void put16(__bf16* o, const uint8_t* s, bool accumulate) {
+  const f32x4 lo = *reinterpret_cast<const f32x4*>(s), hi = *reinterpret_cast<const f32x4*>(s + 16);
+  bf16x8 old = {}, y;
+  if (accumulate) old = *reinterpret_cast<const bf16x8*>(o);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e] = (__bf16)(accumulate ? lo[e] + (float)old[e] : lo[e]);
+    y[4 + e] = (__bf16)(accumulate ? hi[e] + (float)old[4 + e] : hi[e]);
+  }
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, y), reinterpret_cast<u32x4*>(o));
+}
+
+template <typename OUT, typename P>
+__device__ __forceinline__ void store_tile(const P& p, uint8_t* smem, int wave, int lane, OUT* out, long long ld,
+                                           int rows, int cols, bool accumulate) {
+  const int wm = wave & 1, wn = wave >> 1, lk = lane >> 4;
+  constexpr int kLanes = kTile * (int)sizeof(OUT) / 16;      // lanes that a row takes
+  constexpr int kRows = 64 / kLanes;                         // rows of a wave's store
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h * 128 >= rows) break;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          *reinterpret_cast<f32x4*>(smem + ((2 * i + wm) * 16 + (lane & 15)) * kOutStride +
+                                    (u * 128 + wn * 32 + v * 16 + lk * 4) * 4) = p.acc[h][i][u][v];
+    __syncthreads();
+    const int c = lane % kLanes * (16 / (int)sizeof(OUT));
+#pragma unroll 4
+    for (int r = wave * kRows + lane / kLanes; r < 128; r += 8 * kRows)
+      if (h * 128 + r < rows && c < cols)
+        put16(out + (h * 128 + r) * ld + c, smem + r * kOutStride + c * 4, accumulate);
+  }
+}
+
 template <bool A_G, bool B_G>
-__global__ __launch_bounds__(kThreads, 2) void grouped_wgrad_bf16_kernel(moe_wgrad_bf16_args a) {
+__global__ __launch_bounds__(kThreads, 2) void grouped_wgrad_bf16_kernel(WgradParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  const moe_wgrad_bf16_args& a = p.a;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int nt = (a.n + kTile - 1) / kTile, kt = (a.k + kTile - 1) / kTile;
-  const int g = blockIdx.x / (nt * kt), in = blockIdx.x - g * nt * kt;
-  const int m0 = in / kt * kTile, n0 = in % kt * kTile;
-  const int row0 = clampi(a.group_offsets[g], 0, a.total_rows);
-  const int rows = max(clampi(a.group_offsets[g + 1], 0, a.total_rows) - row0, 0);
+  const int nt = (a.n + kTile - 1) / kTile, kt = (a.k + kTile - 1) / kTile, tiles = nt * kt * p.splits;
+  const int per = (tiles + kXcds - 1) / kXcds, slot = blockIdx.x / kXcds;
+  const int g = a.num_groups - 1 - slot / per;
+  const int at = ((blockIdx.x + g) & (kXcds - 1)) * per + slot % per;
+  if (at >= tiles) return;
+  const int split = at / (nt * kt), in = at - split * nt * kt;
+  const int band = in / (kWBand * nt), r = in - band * kWBand * nt, width = min(kWBand, kt - band * kWBand);
+  const int m0 = r / width * kTile, n0 = (band * kWBand + r % width) * kTile;
+  int row0 = clampi(a.group_offsets[g], 0, a.total_rows);
+  int rows = max(clampi(a.group_offsets[g + 1], 0, a.total_rows) - row0, 0);
+  if (p.splits > 1) {          // this part of the rows, in whole steps
+    const int steps = (rows + kStep - 1) / kStep;
+    const int lo = (int)((long long)steps * split / p.splits) * kStep;
+    const int hi = min((int)((long long)steps * (split + 1) / p.splits) * kStep, rows);
+    row0 += lo;
+    rows = hi - lo;
+  }
   Operand A, B;
   const uint8_t* ab = static_cast<const uint8_t*>(a.a) + (long long)m0 * 2;
   const uint8_t* bb = static_cast<const uint8_t*>(a.b) + (long long)n0 * 2;
   A.base = A_G ? ab : ab + (long long)row0 * a.lda * 2;
   B.base = B_G ? bb : bb + (long long)row0 * a.ldb * 2;
-  A.bytes = (uint32_t)(a.a_rows * a.lda * 2 - m0 * 2);
-  B.bytes = (uint32_t)(a.b_rows * a.ldb * 2 - n0 * 2);
+  A.bytes = (uint32_t)((long long)a.a_rows * a.lda * 2 - m0 * 2);
+  B.bytes = (uint32_t)((long long)a.b_rows * a.ldb * 2 - n0 * 2);
   A.index = A_G ? a.a_row_index + row0 : nullptr;
   B.index = B_G ? a.b_row_index + row0 : nullptr;
   A.rows = B.rows = rows;
@@ -703,41 +787,48 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_wgrad_bf16_kernel(moe_wgr
   B.max_row = a.b_rows - 1;
   crossed_offsets(A, wave, lane, (uint32_t)a.lda * 2, a.n - m0, A_G);
   crossed_offsets(B, wave, lane, (uint32_t)a.ldb * 2, a.k - n0, B_G);
-  Product<true, true, A_G, B_G, 4, 4> p(smem, wave, lane, (rows + kStep - 1) / kStep, A, B);
-  p.run();
+  Product<true, true, A_G, B_G, 4, 4> product(smem, wave, lane, (rows + kStep - 1) / kStep, A, B);
+  product.run();
 
-  const int wm = wave & 1, wn = wave >> 1, lk = lane >> 4;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = m0 + h * 128 + (2 * i + wm) * 16 + (lane & 15);
-      if (r >= a.n) continue;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int c = n0 + u * 128 + wn * 32 + v * 16 + lk * 4;
-          if (c >= a.k) continue;
-          const long long at = ((long long)g * a.n + r) * a.k + c;
-          f32x4 x = p.acc[h][i][u][v];
-          if (a.out_dtype == MOE_F32) {
-            f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at);
-            *o = a.accumulate ? x + *o : x;
-          } else {
-            bf16x4* o = reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at);
-            if (a.accumulate) {
-              const bf16x4 old = *o;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] += (float)old[e];
-            }
-            bf16x4 y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
-            *o = y;
-          }
-        }
-    }
+  const int out_rows = min(a.n - m0, kTile), out_cols = min(a.k - n0, kTile);
+  if (p.splits > 1)
+    store_tile(product, smem, wave, lane, p.part + (((long long)split * a.num_groups + g) * a.n + m0) * a.k + n0, a.k,
+               out_rows, out_cols, false);
+  else if (a.out_dtype == MOE_F32)
+    store_tile(product, smem, wave, lane, static_cast<float*>(a.out) + ((long long)g * a.n + m0) * a.k + n0, a.k,
+               out_rows, out_cols, a.accumulate);
+  else
+    store_tile(product, smem, wave, lane, static_cast<__bf16*>(a.out) + ((long long)g * a.n + m0) * a.k + n0, a.k,
+               out_rows, out_cols, a.accumulate);
+}
+
+// out = (out +) the sum of the parts, eight values a thread.
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* part, int splits, long long values, void* out,
+                                                          moe_dtype_t dt, int accumulate) {
+  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (at >= values) return;
+  f32x4 x[2] = {};
+  for (int s = 0; s < splits; ++s) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(part + s * values + at);
+    x[0] += q[0];
+    x[1] += q[1];
+  }
+  if (dt == MOE_F32) {
+    put16(static_cast<float*>(out) + at, reinterpret_cast<const uint8_t*>(x), accumulate);
+    put16(static_cast<float*>(out) + at + 4, reinterpret_cast<const uint8_t*>(x + 1), accumulate);
+  } else {
+    put16(static_cast<__bf16*>(out) + at, reinterpret_cast<const uint8_t*>(x), accumulate);
+  }
+}
+
+// Parts that a group's rows are cut into: with fewer tiles than half the
+// compute units, as many as fill them, of at least 512 rows on average.
+int wgrad_splits(int num_groups, int total_rows, int n, int k) {
+  const long long tiles = (long long)num_groups * ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
+  if (tiles == 0 || tiles > 128) return 1;
+  const long long fill = 256 / tiles, deep = total_rows / num_groups / 512;
+  const long long s = fill < deep ? fill : deep;
+  return s > 1 ? (int)s : 1;
 }
 
 bool valid_dt(moe_dtype_t d) { return d == MOE_BF16 || d == MOE_F32; }
@@ -791,7 +882,9 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hi
 
 extern "C" size_t moe_grouped_wgrad_bf16_workspace_bytes(int num_groups, int total_rows, int n,
                                                          int k) {
-  return 0;
+  if (num_groups < 1 || total_rows < 0 || n < 0 || k < 0) return 0;
+  const int s = wgrad_splits(num_groups, total_rows, n, k);
+  return s > 1 ? (size_t)s * num_groups * n * k * sizeof(float) : 0;
 }
 
 extern "C" moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, void* ws,
@@ -811,18 +904,31 @@ extern "C" moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, 
   if (a.n == 0 || a.k == 0) return MOE_OK;
   if (!a.group_offsets || !a.out || (a.total_rows > 0 && (!a.a || !a.b))) return MOE_ERR_NULL;
   if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.out)) return MOE_ERR_ALIGN;
-  if (ws_bytes < moe_grouped_wgrad_bf16_workspace_bytes(a.num_groups, a.total_rows, a.n, a.k))
-    return MOE_ERR_WORKSPACE;
-  const long long tiles = (long long)a.num_groups * ((a.n + kTile - 1) / kTile) * ((a.k + kTile - 1) / kTile);
-  if (tiles > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
+  const int splits = wgrad_splits(a.num_groups, a.total_rows, a.n, a.k);
+  if (splits > 1) {
+    if (!ws || ws_bytes < moe_grouped_wgrad_bf16_workspace_bytes(a.num_groups, a.total_rows, a.n, a.k))
+      return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGN;
+  }
+  const long long tiles = (long long)((a.n + kTile - 1) / kTile) * ((a.k + kTile - 1) / kTile) * splits;
+  const long long grid = a.num_groups * ((tiles + kXcds - 1) / kXcds * kXcds);
+  if (grid > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
   if (moe_status_t s = check_device()) return s;
-  static void (*const table[2][2])(moe_wgrad_bf16_args) = {
+  static void (*const table[2][2])(WgradParams) = {
       {grouped_wgrad_bf16_kernel<false, false>, grouped_wgrad_bf16_kernel<false, true>},
       {grouped_wgrad_bf16_kernel<true, false>, grouped_wgrad_bf16_kernel<true, true>}};
-  const int ga = a.a_row_index != nullptr, gb = a.b_row_index != nullptr;
+  const int ga = a.a_row_index && a.total_rows > 0, gb = a.b_row_index && a.total_rows > 0;
   static std::atomic<uint64_t> lds_set[2][2] = {};
   if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(table[ga][gb]), kLds, lds_set[ga][gb]))
     return st;
-  hipLaunchKernelGGL(table[ga][gb], dim3((unsigned)tiles), dim3(kThreads), kLds, stream, a);
-  return launch_status();
+  const WgradParams p{a, splits, static_cast<float*>(ws)};
+  hipLaunchKernelGGL(table[ga][gb], dim3((unsigned)grid), dim3(kThreads), kLds, stream, p);
+  if (moe_status_t s = launch_status()) return s;
+  if (splits > 1) {
+    const long long values = (long long)a.num_groups * a.n * a.k;
+    hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)((values / 8 + 255) / 256)), dim3(256), 0, stream,
+                       static_cast<const float*>(ws), splits, values, a.out, a.out_dtype, a.accumulate);
+    return launch_status();
+  }
+  return MOE_OK;
 }

@@ -333,6 +333,27 @@ def test_grouped_wgrad_bf16(moe, case):
     _close(got, want, UB[out] * np.abs(want) + (max(sizes) + 8) * 2.0 ** -23 * mag, "dW")
 
 
+def test_grouped_wgrad_bf16_many_tiles(moe):
+    """More tiles than compute units hold at once, of groups with none to many
+    steps, gathered on both sides."""
+    rng = np.random.default_rng(12)
+    sizes = [1, 70, 0, 200, 333, 64, 65, 0, 128, 5, 257, 90, 31, 0, 190, 12] * 2
+    off = _offsets(sizes)
+    R, n, k = int(off[-1]), 1032, 1544
+    a, b = _make(rng, (150, n), "bf16"), _make(rng, (140, k), "bf16")
+    ia, ib = (rng.integers(0, m, R).astype(np.int32) for m in (150, 140))
+    want, mag = train.grouped_wgrad(a[1], b[1], off, ia, ib)
+    log("moe_grouped_wgrad_bf16 many tiles")
+    for out in ("f32", "bf16"):
+        dt = torch.float32 if out == "f32" else torch.bfloat16
+        got = moe.moe_grouped_wgrad_bf16(a[0], b[0], to_dev(off), R, to_dev(ia), to_dev(ib),
+                                         out_dtype=dt)
+        _close(got, want, UB[out] * np.abs(want) + (max(sizes) + 8) * 2.0 ** -23 * mag, out)
+    again = moe.moe_grouped_wgrad_bf16(a[0], b[0], to_dev(off), R, to_dev(ia), to_dev(ib),
+                                       out_dtype=torch.bfloat16)
+    assert torch.equal(got, again)
+
+
 def test_grouped_wgrad_bf16_long_single_group_is_deterministic(moe):
     rng = np.random.default_rng(11)
     R, n, k = 5000, 64, 136
@@ -344,6 +365,15 @@ def test_grouped_wgrad_bf16_long_single_group_is_deterministic(moe):
     assert torch.equal(got, again)
     want, mag = train.grouped_wgrad(a[1], b[1], [0, R])
     _close(got, want, UB["f32"] * np.abs(want) + (R + 8) * 2.0 ** -23 * mag, "dW")
+    old = _make(rng, (1, n, k), "bf16")
+    got = moe.moe_grouped_wgrad_bf16(a[0], b[0], off, R, accumulate=True, out=old[0].clone())
+    want, mag = want + old[1], mag + np.abs(old[1])
+    _close(got, want, UB["bf16"] * np.abs(want) + (R + 8) * 2.0 ** -23 * mag, "dW, added")
+    off2 = _offsets([2100, 0, 2900])        # two parts a group, one group without rows
+    ia = rng.integers(0, R, R).astype(np.int32)
+    got = moe.moe_grouped_wgrad_bf16(a[0], b[0], to_dev(off2), R, a_row_index=to_dev(ia))
+    want, mag = train.grouped_wgrad(a[1], b[1], off2, ia)
+    _close(got, want, UB["f32"] * np.abs(want) + (R + 8) * 2.0 ** -23 * mag, "dW, ragged parts")
 
 
 # ---------------------------------------------------------------------------

@@ -95,6 +95,16 @@ def test_grouped_wgrad_arguments(lib, change, status):
                                       None) == status
 
 
+def test_grouped_wgrad_workspace(lib):
+    need = lib.moe_grouped_wgrad_bf16_workspace_bytes
+    assert need(33, 16384, 4096, 7168) == 0             # tiles enough for every compute unit
+    assert need(1, 8192, 256, 7168) > 0 and need(1, 100, 256, 7168) == 0
+    assert need(0, 8192, 256, 256) == 0 and need(1, 8192, 0, 256) == 0
+    long = dict(a_rows=8192, b_rows=8192, total_rows=8192, num_groups=1)
+    assert lib.moe_grouped_wgrad_bf16(_args(moe.WgradBf16Args, WGRAD, **long), None, 0, None) == 4
+    assert lib.moe_grouped_wgrad_bf16(_args(moe.WgradBf16Args, WGRAD, **long), 24, 1 << 30, None) == 3
+
+
 def test_swiglu_arguments(lib):
     f = lambda a=P16, dt=0, R=4, I=8, lda=16, h=P16, ldh=8: lib.moe_swiglu(  # noqa: E731
         a, dt, R, I, lda, h, ldh, None)
