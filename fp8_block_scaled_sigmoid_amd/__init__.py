@@ -134,7 +134,7 @@ def lib():
             "moe_layer_forward": [ctypes.POINTER(LayerArgs), _P, ctypes.c_size_t, _P],
             "moe_block_norm": [ctypes.POINTER(BlockNormArgs), _P],
             "moe_block_norm_backward": [ctypes.POINTER(BlockNormBwdArgs), _P, _SZ, _P],
-            "moe_grouped_gemm_bf16": [ctypes.POINTER(GemmBf16Args), _P],
+            "moe_grouped_gemm_bf16": [ctypes.POINTER(GemmBf16Args), _P, _SZ, _P],
             "moe_grouped_wgrad_bf16": [ctypes.POINTER(WgradBf16Args), _P, _SZ, _P],
             "moe_swiglu": [_P, _I, _I, _I, _LL, _P, _LL, _P],
             "moe_swiglu_backward": [_P, _P, _I, _I, _I, _LL, _LL, _P, _P, _LL, _P, _P, _LL, _P],
@@ -157,6 +157,8 @@ def lib():
         L.moe_layer_workspace_bytes.restype = ctypes.c_size_t
         L.moe_block_norm_backward_workspace_bytes.argtypes = [_I, _I]
         L.moe_block_norm_backward_workspace_bytes.restype = _SZ
+        L.moe_grouped_gemm_bf16_workspace_bytes.argtypes = [_I, _I, _I, _I]
+        L.moe_grouped_gemm_bf16_workspace_bytes.restype = _SZ
         L.moe_grouped_wgrad_bf16_workspace_bytes.argtypes = [_I, _I, _I, _I]
         L.moe_grouped_wgrad_bf16_workspace_bytes.restype = _SZ
         L.moe_grad_table_bytes.argtypes = [_I]
@@ -691,8 +693,13 @@ def moe_block_norm_backward(r, dr=None, dh=None, b=None, w_pre=None, w_post=None
     return dx, db, dw_pre, dw_post, dgate
 
 
+def moe_grouped_gemm_bf16_workspace_bytes(G, total_rows, n_out, k_dim):
+    return int(lib().moe_grouped_gemm_bf16_workspace_bytes(G, total_rows, n_out, k_dim))
+
+
 def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_index=None,
-                          row_scale=None, out=None, out_dtype=torch.bfloat16, stream=None):
+                          row_scale=None, out=None, out_dtype=torch.bfloat16, ws=None,
+                          stream=None):
     """Grouped bf16 product: out[r] = row_scale[r] * A[src(r)] @ B[g]^T for the
     rows r of each group, b bf16 [G, n_out, K]; with b_kn, A[src(r)] @ B[g], b
     [G, K, n_out] (the input gradient, from the forward product's weights).
@@ -712,7 +719,11 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
                         b.data_ptr(), MOE_B_KN if b_kn else MOE_B_NK, group_offsets.data_ptr(), G,
                         total_rows, n, K, _dtype_code(out, "out"), op, ldo,
                         _vector(row_scale, total_rows, "row_scale"))
-    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(ctypes.byref(args), _queue(stream)))
+    need = moe_grouped_gemm_bf16_workspace_bytes(G, total_rows, n, K)
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+    _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(
+        ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _queue(stream)))
     return out
 
 

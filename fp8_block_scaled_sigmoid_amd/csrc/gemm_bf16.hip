@@ -47,6 +47,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef const __attribute__((address_space(4))) int32_t* uniform_int_t;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
 
 constexpr int kMaxGroups = 1025;
@@ -541,79 +542,146 @@ __device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
 
 // The tile list of the large-batch kernel.  A group's rows are cut into tiles of
 // 256 and a rest, in bands of up to kBand row tiles, column tile by column
-// tile, so that tiles which share a weight tile follow one another.  32
-// consecutive tiles, one round of an XCD's compute units, form a run and go to
-// one XCD: they share a few row and column tiles through its L2.  Runs are
-// dispatched in the order of a golden-ratio stride over the list, not in list
-// order: a group with many rows needs the matrix cores and hardly any
-// memory, one with few rows the reverse, and this way every moment has some
-// of both (in list order the groups' weights arrive at the memory's rate while
-// the matrix cores wait).
+// tile, so that tiles which share a weight tile follow one another.  kRun
+// consecutive tiles, one round of an XCD's compute units (fewer where that
+// would leave XCDs without any), form a run; run j of
+// the dispatch order belongs to XCD j % 8, and its tiles share a few row and
+// column tiles through that XCD's L2.  Runs are dispatched in the order of a
+// golden-ratio stride over the list, not in list order: a group with many
+// rows needs the matrix cores and hardly any memory, one with few rows the
+// reverse, and this way every moment has some of both (in list order the
+// groups' weights arrive at the memory's rate while the matrix cores wait).
+//
+// The grid is one workgroup per compute unit.  A workgroup's first tile is its
+// own by position; further ones come from its XCD's counter and, when that
+// XCD's runs are all taken, from the next XCD's: tiles differ in time by a
+// factor of two, and workgroups that the hardware hands out one per tile
+// leave a tenth of the compute units waiting.
+constexpr int kXcds = 8;
 constexpr int kBand = 4;
 constexpr int kRun = 32;
 constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;      // groups of a thread
+constexpr int kCounterStride = 16;                                // ints between the XCDs' counters
+constexpr int kListAt = kLds;                                     // behind the half tiles: row tiles before group g
+constexpr int kNextAt = kListAt + (kMaxGroups + 1) * 4;           // and the next position, the group found
+constexpr int kListLds = (kNextAt + 16 + 15) / 16 * 16;
 
-__device__ __forceinline__ bool find_tile(const moe_gemm_bf16_args& a, int* tmp, TileAt& t) {
-  const int G = a.num_groups, n_tiles = (a.n_out + kTile - 1) / kTile;
-  int lo[kPer], n[kPer], sum = 0, all;
-  const int per = (G + kThreads - 1) / kThreads;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    n[i] = i < per ? group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo[i]) : 0;
-    sum += (n[i] + kTile - 1) / kTile;
-  }
-  int at = prefix(sum, tmp, all) * n_tiles;
-  // the workgroup's place: run j of the dispatch order, tile `in` of it
-  const int slot = blockIdx.x >> 3, xcd = blockIdx.x & 7;
-  const int runs = (all * n_tiles + kRun - 1) / kRun;
-  const int j = slot / kRun * 8 + xcd;
-  if (j >= runs) return false;
-  int stride = max((int)(0.618034f * runs), 1);
-  for (;; ++stride) {               // the next one that has no factor in common with the runs
-    int x = runs, y = stride;
-    while (y) {
-      const int r = x % y;
-      x = y;
-      y = r;
-    }
-    if (x == 1) break;
-  }
-  const int want = (int)((long long)j * stride % runs) * kRun + slot % kRun;
-  if (want >= all * n_tiles) return false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int mt = (n[i] + kTile - 1) / kTile;
-    const int in = want - at;
-    if (in >= 0 && in < mt * n_tiles) {
-      const int band = in / (kBand * n_tiles), rest = in - band * kBand * n_tiles;
-      const int height = min(kBand, mt - band * kBand);
-      const int n_tile = rest / height;
-      const int m = band * kBand + rest - n_tile * height;
-      tmp[8] = (int)threadIdx.x * per + i, tmp[9] = lo[i], tmp[10] = m * kTile, tmp[11] = n[i] - m * kTile;
-      tmp[12] = n_tile;
-    }
-    at += mt * n_tiles;
-  }
-  __syncthreads();
-  t.g = __builtin_amdgcn_readfirstlane(tmp[8]);
-  t.row0 = __builtin_amdgcn_readfirstlane(tmp[9]);
-  t.m0 = __builtin_amdgcn_readfirstlane(tmp[10]);
-  t.m_rows = min(__builtin_amdgcn_readfirstlane(tmp[11]), kTile);
-  t.n0 = __builtin_amdgcn_readfirstlane(tmp[12]) * kTile;
-  t.cols = min(kTile, a.n_out - t.n0);
-  return true;
+struct GemmParams {
+  moe_gemm_bf16_args a;
+  unsigned* next;          // [8] counters, NULL when the first tiles are all
+};
+
+__global__ void tile_counters_kernel(unsigned* next, unsigned first) {
+  if (threadIdx.x < kXcds) next[threadIdx.x * kCounterStride] = first;
 }
 
+struct TileList {
+  const moe_gemm_bf16_args& a;
+  const int* before;       // LDS
+  int* shared;             // LDS: the next position, the group found
+  unsigned* next;
+  int n_tiles, tiles, run, runs, stride;      // run: its tiles
+  int home, xcd;           // the workgroup's XCD; the one whose list it takes from
+
+  __device__ __forceinline__ TileList(const GemmParams& p, uint8_t* smem, int* tmp)
+      : a(p.a), before(reinterpret_cast<int*>(smem + kListAt)), shared(reinterpret_cast<int*>(smem + kNextAt)),
+        next(p.next) {
+    const int G = a.num_groups, per = (G + kThreads - 1) / kThreads;
+    int* list = reinterpret_cast<int*>(smem + kListAt);
+    int lo, mt[kPer], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      mt[i] = i < per ? (group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo) + kTile - 1) / kTile : 0;
+      sum += mt[i];
+    }
+    int at = prefix(sum, tmp, all);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i < per && (int)threadIdx.x * per + i < G) list[(int)threadIdx.x * per + i] = at;
+      at += mt[i];
+    }
+    if (threadIdx.x == 0) list[G] = all;
+    __syncthreads();
+    n_tiles = (a.n_out + kTile - 1) / kTile;
+    tiles = all * n_tiles;
+    run = min(kRun, max((tiles + kXcds - 1) / kXcds, 1));
+    runs = (tiles + run - 1) / run;
+    stride = max((int)(0.618034f * runs), 1);
+    for (;; ++stride) {               // the next one that has no factor in common with the runs
+      int x = runs, y = stride;
+      while (y) {
+        const int r = x % y;
+        x = y;
+        y = r;
+      }
+      if (x <= 1) break;
+    }
+    home = xcd = blockIdx.x & (kXcds - 1);
+  }
+  // The tile at position `slot` of the current XCD's list, or at a later one
+  // of this list and the others; false when there is none.
+  __device__ __forceinline__ bool find(int slot, TileAt& t) {
+    for (;;) {
+      const int j = slot / run * kXcds + xcd;
+      if (j < runs) {
+        const int want = (int)((long long)j * stride % runs) * run + slot % run;
+        if (want < tiles) {
+          const int row_tile = want / n_tiles;
+          for (int g = threadIdx.x; g < a.num_groups; g += kThreads)
+            if (before[g] <= row_tile && row_tile < before[g + 1]) shared[1] = g;
+          __syncthreads();
+          t.g = __builtin_amdgcn_readfirstlane(shared[1]);
+          const int first = __builtin_amdgcn_readfirstlane(before[t.g]);
+          const int mt = __builtin_amdgcn_readfirstlane(before[t.g + 1]) - first;
+          const int in = want - first * n_tiles;
+          const int band = in / (kBand * n_tiles), rest = in - band * kBand * n_tiles;
+          const int height = min(kBand, mt - band * kBand);
+          const int n_tile = rest / height;
+          const uniform_int_t offsets = (uniform_int_t)(uintptr_t)a.group_offsets;
+          t.row0 = clampi(offsets[t.g], 0, a.total_rows);
+          const int rows = clampi(offsets[t.g + 1], 0, a.total_rows) - t.row0;
+          t.m0 = (band * kBand + rest - n_tile * height) * kTile;
+          t.m_rows = min(rows - t.m0, kTile);
+          t.n0 = n_tile * kTile;
+          t.cols = min(kTile, a.n_out - t.n0);
+          return true;
+        }
+      } else {
+        xcd = (xcd + 1) & (kXcds - 1);
+        if (xcd == home) return false;
+      }
+      if (!next) return false;
+      slot = pop_now();
+    }
+  }
+  __device__ __forceinline__ unsigned pop() {
+    // (an increment, because the compiler wraps a wave-wide reduction around an
+    // addition, and that would wait for the result at once)
+    return next && threadIdx.x == 0 ? atomicInc(next + xcd * kCounterStride, 0x7FFFFFFFu) : 0u;
+  }
+  __device__ __forceinline__ int publish(unsigned position) {
+    __syncthreads();
+    if (threadIdx.x == 0) shared[0] = (int)position;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(shared[0]);
+  }
+  __device__ __forceinline__ int pop_now() { return publish(pop()); }
+};
+
 template <bool KN>
-__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(moe_gemm_bf16_args a) {
+__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(GemmParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  TileList list(p, smem, reinterpret_cast<int*>(smem));
   TileAt t;
-  if (!find_tile(a, reinterpret_cast<int*>(smem), t)) return;
-  __syncthreads();        // the list's scratch becomes the first half tile
-  const int l1 = (t.m_rows - 128 + 31) / 32;
-  if (t.m_rows <= 128) short_tile<KN>(a, t, smem);
-  else if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(a, t, smem) : gemm_tile<KN, 4, 3>(a, t, smem);
-  else l1 > 1 ? gemm_tile<KN, 4, 2>(a, t, smem) : gemm_tile<KN, 4, 1>(a, t, smem);
+  for (int slot = blockIdx.x / kXcds; list.find(slot, t);) {
+    const unsigned popped = list.pop();
+    const int l1 = (t.m_rows - 128 + 31) / 32;
+    if (t.m_rows <= 128) short_tile<KN>(p.a, t, smem);
+    else if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(p.a, t, smem) : gemm_tile<KN, 4, 3>(p.a, t, smem);
+    else l1 > 1 ? gemm_tile<KN, 4, 2>(p.a, t, smem) : gemm_tile<KN, 4, 1>(p.a, t, smem);
+    if (!p.next) return;
+    slot = list.publish(popped);      // and all waves are done with LDS
+  }
 }
 
 // Small groups: the time is the weights' stream, so every workgroup (one per
@@ -624,8 +692,9 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(moe_gemm
 // about equal width inside one group.
 
 template <bool KN>
-__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(moe_gemm_bf16_args a) {
+__global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(GemmParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  const moe_gemm_bf16_args& a = p.a;
   int* tmp = reinterpret_cast<int*>(smem);
   constexpr int kUnit = KN ? 64 : 16;
   const int G = a.num_groups, units = (a.n_out + kUnit - 1) / kUnit;
@@ -694,7 +763,6 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(m
 //     first.
 // Where there are few tiles, each group's rows are cut into `splits` parts,
 // whose partial sums (float, in the workspace) a second kernel adds in order.
-constexpr int kXcds = 8;
 constexpr int kWBand = 4;
 constexpr int kOutStride = kTile * 4 + 16;      // bytes between rows staged in LDS, off the banks' period
 static_assert(128 * kOutStride <= kLds, "half a tile of float rows fits");
@@ -831,6 +899,20 @@ int wgrad_splits(int num_groups, int total_rows, int n, int k) {
   return s > 1 ? (int)s : 1;
 }
 
+// Row tiles of 256 that the groups can make at most.
+long long row_tiles(int num_groups, int total_rows) {
+  return (long long)total_rows / kTile + (num_groups < total_rows ? num_groups : total_rows);
+}
+// Up to 64 rows a group on average the weights' stream decides: 64 rows over
+// 33 groups of 4096 x 7168 take 343 us there and 384 with a workgroup per tile;
+// at 124 rows both take 430 to 450, at 182 the stream kernel 547 against 454.
+bool streams_weights(int num_groups, int total_rows) { return total_rows <= 64LL * num_groups; }
+// Workgroups of an XCD: one per compute unit (of the whole chip without a device).
+int places() {
+  const int cus = cu_count();
+  return cus < kXcds ? 32 : cus / kXcds;
+}
+
 bool valid_dt(moe_dtype_t d) { return d == MOE_BF16 || d == MOE_F32; }
 // element rows that 32-bit byte offsets of a gathered operand can reach
 bool fits31(long long rows, long long ld) { return rows * ld * 2 < (1LL << 31); }
@@ -839,7 +921,17 @@ bool tile_fits31(long long ld) { return fits31(kTile, ld); }
 
 }  // namespace
 
-extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hipStream_t stream) {
+extern "C" size_t moe_grouped_gemm_bf16_workspace_bytes(int num_groups, int total_rows, int n_out,
+                                                        int k_dim) {
+  (void)k_dim;
+  if (num_groups < 1 || total_rows < 1 || n_out < 1 || streams_weights(num_groups, total_rows)) return 0;
+  const long long tiles = row_tiles(num_groups, total_rows) * ((n_out + kTile - 1) / kTile);
+  if (tiles <= kXcds * kRun && places() >= kRun) return 0;      // every tile is some workgroup's first
+  return kXcds * kCounterStride * sizeof(unsigned);
+}
+
+extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, void* ws, size_t ws_bytes,
+                                              hipStream_t stream) {
   if (!args) return MOE_ERR_NULL;
   const moe_gemm_bf16_args& a = *args;
   if (a.total_rows < 0 || a.n_out < 0 || a.k_dim < 0 || a.n_out % 8 || a.k_dim % 8 ||
@@ -855,28 +947,26 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hi
   if (a.a_rows == 0) return MOE_ERR_SHAPE;
   if (!a.group_offsets || !a.out || (a.k_dim > 0 && (!a.a || !a.b))) return MOE_ERR_NULL;
   if (!aligned16(a.a) || !aligned16(a.b) || !aligned16(a.out)) return MOE_ERR_ALIGN;
+  const size_t need = moe_grouped_gemm_bf16_workspace_bytes(a.num_groups, a.total_rows, a.n_out, a.k_dim);
+  if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need && !aligned16(ws)) return MOE_ERR_ALIGN;
+  if (row_tiles(a.num_groups, a.total_rows) * ((a.n_out + kTile - 1) / kTile) > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (moe_status_t s = check_device()) return s;
-  const bool kn = a.b_layout == MOE_B_KN;
-  const bool stream_weights = a.total_rows <= 64LL * a.num_groups;
-  long long grid;
-  if (stream_weights) {
-    grid = cu_count();
-    if (grid < 1) grid = 256;
-  } else {
-    const long long tiles = ((long long)a.total_rows / kTile +
-                             (a.num_groups < a.total_rows ? a.num_groups : a.total_rows)) *
-                            ((a.n_out + kTile - 1) / kTile);
-    grid = (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun);
-    if (grid > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
+  const bool kn = a.b_layout == MOE_B_KN, stream_weights = streams_weights(a.num_groups, a.total_rows);
+  const int grid = places() * kXcds;
+  const GemmParams p{a, need ? static_cast<unsigned*>(ws) : nullptr};
+  if (need) {
+    hipLaunchKernelGGL(tile_counters_kernel, dim3(1), dim3(64), 0, stream, p.next, (unsigned)grid / kXcds);
+    if (moe_status_t s = launch_status()) return s;
   }
-  static void (*const table[2][2])(moe_gemm_bf16_args) = {
+  static void (*const table[2][2])(GemmParams) = {
       {grouped_gemm_bf16_kernel<false>, grouped_gemm_bf16_kernel<true>},
       {grouped_gemm_bf16_stream_kernel<false>, grouped_gemm_bf16_stream_kernel<true>}};
   static std::atomic<uint64_t> lds_set[2][2] = {};
   const auto kernel = table[stream_weights][kn];
-  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), kLds, lds_set[stream_weights][kn]))
+  if (moe_status_t st = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), kListLds, lds_set[stream_weights][kn]))
     return st;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kThreads), kLds, stream, a);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), kListLds, stream, p);
   return launch_status();
 }
 

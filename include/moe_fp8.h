@@ -563,7 +563,10 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* args, void* 
  * group_offsets int32 [G+1] on the device, non-decreasing, first 0 and last
  * total_rows (values outside [0, total_rows] are clamped); groups may be empty;
  * gathered indices are clamped to a_rows.  Products are summed in float in an
- * order that depends on the sizes alone.
+ * order that depends on the sizes alone.  ws: device scratch, 16-byte aligned, of
+ * moe_grouped_gemm_bf16_workspace_bytes(...) bytes (counters that workgroups take
+ * their tiles from; may be NULL when that is 0); calls that share it must be
+ * ordered on one stream.
  * Requires k_dim, n_out, lda, ldo multiples of 8, lda >= k_dim, ldo >= n_out, and
  * a_rows >= total_rows without a_row_index (MOE_ERR_SHAPE); a, b, out 16-byte
  * aligned; 1 <= G <= 1025, n_out * k_dim < 2^30, and with a_row_index
@@ -583,7 +586,9 @@ typedef struct {
   const float* row_scale;
 } moe_gemm_bf16_args;
 
-moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, hipStream_t stream);
+size_t moe_grouped_gemm_bf16_workspace_bytes(int num_groups, int total_rows, int n_out, int k_dim);
+moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
 
 /*
  * Weight gradients of the same groups:

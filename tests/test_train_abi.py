@@ -22,6 +22,7 @@ def test_declared_and_exported(lib):
     names = declared_functions()
     for n in ("moe_block_norm", "moe_block_norm_backward",
               "moe_block_norm_backward_workspace_bytes", "moe_grouped_gemm_bf16",
+              "moe_grouped_gemm_bf16_workspace_bytes",
               "moe_grouped_wgrad_bf16", "moe_grouped_wgrad_bf16_workspace_bytes", "moe_swiglu",
               "moe_swiglu_backward", "moe_grad_table_bytes", "moe_grad_table",
               "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_scale", "moe_grad_clip"):
@@ -78,7 +79,18 @@ GEMM = dict(a=P16, lda=16, a_rows=4, b=P16, group_offsets=P16, num_groups=2, tot
     (dict(group_offsets=None), 1), (dict(out=None), 1), (dict(b=24), 3), (dict(total_rows=0), 0),
     (dict(n_out=0), 0)])
 def test_grouped_gemm_arguments(lib, change, status):
-    assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **change), None) == status
+    assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **change), None, 0, None) == status
+
+
+def test_grouped_gemm_workspace(lib):
+    need = lib.moe_grouped_gemm_bf16_workspace_bytes
+    assert need(33, 144, 4096, 7168) == 0           # few rows a group: the weights' stream
+    assert need(1, 1000, 1024, 512) == 0            # a tile for every workgroup at most
+    assert need(33, 16384, 4096, 7168) > 0
+    assert need(0, 16384, 4096, 7168) == 0 and need(33, 0, 4096, 7168) == 0
+    many = dict(a_rows=1 << 17, total_rows=1 << 17, n_out=1024, ldo=1024)
+    assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **many), None, 0, None) == 4
+    assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **many), 24, 512, None) == 3
 
 
 WGRAD = dict(a=P16, lda=8, a_rows=4, b=P16, ldb=16, b_rows=4, group_offsets=P16, num_groups=2,
