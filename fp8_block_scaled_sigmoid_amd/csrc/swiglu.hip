@@ -5,6 +5,10 @@
 // gradient of the expert row before the gate):
 //   dg = w dh u (s + silu(g) (1 - s)),  du = w dh silu(g),  dw = sum_c h dh
 // and w h, the rows that the weight gradient of the second product reads.
+//
+// Memory bounds both: 3 values an element pair forward (two read, one written),
+// 6 backward.  The backward pass at 73728 x 2048 in bf16 moves 1.81 GB in 317 us,
+// 5.7 TB/s; the forward kernel takes 2.9 us at 9 x 2048.
 #include "rows.h"
 
 namespace {
@@ -96,6 +100,12 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(BwdParams p) {
   if (live && tid == first * 64) p.dgate[row] = sum;
 }
 
+// A wave takes 512 columns at a time; a row gets the waves that it fills with
+// one vector a thread, up to the workgroup's four.  At 2048 columns and 32768 rows
+// one, two and four waves a row take 150, 144 and 142 us (at 9 rows 7.6, 6.8 and
+// 7.0), at 512 columns 31.3, 33.4 and 45.5.
+int waves_of_row(int I) { return I > 1024 ? 4 : (I > 512 ? 2 : 1); }
+
 }  // namespace
 
 extern "C" moe_status_t moe_swiglu(const void* a, moe_dtype_t dt, int R, int I, long long lda,
@@ -140,7 +150,7 @@ extern "C" moe_status_t moe_swiglu_backward(const void* a, const void* dh, moe_d
     return MOE_ERR_ALIGN;
   if (moe_status_t s = check_device()) return s;
   const BwdParams p{a, dh, row_gate, da, hg, dgate, lda, lddh, ldda, ldhg, R, I,
-                    R >= 8192 ? 1 : (R >= 4096 ? 2 : 4)};
+                    waves_of_row(I)};
   const int rows = 4 / p.wpr;
   const dim3 grid((unsigned)((R + (long long)rows - 1) / rows));
   if (dt == MOE_BF16)
