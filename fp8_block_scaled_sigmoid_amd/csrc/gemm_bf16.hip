@@ -27,9 +27,9 @@
 //     [128 columns], swizzled for ds_read_b64_tr_b16, which hands each lane
 //     four k values of its column.
 //   * A tile of fewer than 256 rows skips the MFMAs of its empty subtiles (the
-//     loop is compiled for each count); one of at most 128 rows has no second
-//     half of A, and runs two phases a step over three steps in LDS
-//     (ShortProduct).
+//     loop is compiled for each count); one of up to 288 carries 32 rows behind
+//     A's halves; one of at most 128 has no second half of A, and runs two
+//     phases a step over three steps in LDS (ShortProduct).
 //   * Rows past a group's end, columns past the matrix and the tail of k are
 //     given offsets beyond the buffer resource's size and read as zero, so
 //     they never meet the group's data, whatever they hold.
@@ -53,9 +53,11 @@ typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
 constexpr int kMaxGroups = 1025;
 constexpr int kThreads = 512;
 constexpr int kTile = 256;                 // rows and columns of a tile
+constexpr int kUnit = 32;                  // row tiles are multiples of this, up to kTile + kUnit
 constexpr int kStep = 64;                  // contraction depth of a step
 constexpr int kHalf = 128 * kStep * 2;     // bytes of a half tile
-constexpr int kLds = 9 * kHalf;            // [A, B][half][step parity], or 3 x [A, B0, B1]
+// [A, B][half][step parity] and 32 more rows of A twice, or 3 x [A, B0, B1]
+constexpr int kLds = 9 * kHalf;
 constexpr uint32_t kOut = 0x80000000u;     // an offset past every buffer (all are below 2^31)
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
@@ -70,6 +72,7 @@ struct Operand {
   uint32_t bytes;          // straight, gathered: size of the resource
   uint32_t off[2][2];      // [half][j]: this lane's offsets of its two loads of a half tile
   uint32_t tail;           // straight: added to the offsets in the last step
+  uint32_t extra;          // straight: the offset of the load of the extra rows
   // crossed
   const int32_t* index;    // gather, from the group's first row
   int rows, max_row;       // contraction length; last row of a gathered operand
@@ -99,6 +102,7 @@ __device__ __forceinline__ void barrier() {
 template <bool A_X, bool B_X>
 struct Tile {
   f32x4 acc[2][4][2][2];        // [A half][subtile][B half][subtile]
+  f32x4 more[2][2];             // [B half][subtile] of the rows past A's halves
   uint8_t* smem;
   int wave, lane, n_steps;
   const Operand &A, &B;
@@ -190,6 +194,16 @@ struct Tile {
     __builtin_amdgcn_s_setprio(0);
   }
 
+  __device__ __forceinline__ void extra(const bf16x8 (&a)[2], const bf16x8 (&b)[2][2], int hb) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        more[hb][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[t][kk], a[kk], more[hb][t], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  }
+
   template <int H, int L>
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -202,18 +216,31 @@ struct Tile {
 };
 
 // The K loop.  A_G / B_G: gathered crossed operand; L0, L1: 16-row subtiles per
-// wave with rows in A's first and second half.
-template <bool A_X, bool B_X, bool A_G, bool B_G, int L0, int L1>
+// wave with rows in A's first and second half.  EXTRA: kUnit more rows of a
+// straight A, copied together with its second half and multiplied in phase 2.
+// (Their 16 accumulators and fragments make the compiler put seven loop
+// invariants into scratch; with their second half of the work in phase 3 it is
+// 15, and the time the same.)
+template <bool A_X, bool B_X, bool A_G, bool B_G, int L0, int L1, bool EXTRA = false>
 struct Product : Tile<A_X, B_X> {
   using T = Tile<A_X, B_X>;
   using T::A, T::B, T::smem, T::wave, T::n_steps;
   static constexpr int kIdx = 2 * (A_G ? 1 : 0) + 2 * (B_G ? 1 : 0);   // index loads a step
-  bf16x8 a0[4][2], a1[4][2], b0[2][2], b1[2][2];
+  static constexpr int kMore = EXTRA ? 1 : 0;                          // copies of the extra rows
+  bf16x8 a0[4][2], a1[4][2], a2[2], b0[2][2], b1[2][2];
   int ia[2][2], ib[2][2];       // gathered rows of the two steps ahead, [step parity][j]
   using T::T;
 
   __device__ __forceinline__ uint8_t* slot(int op, int h, int par) {
     return smem + ((op * 2 + h) * 2 + par) * kHalf;
+  }
+
+  __device__ __forceinline__ uint8_t* extra_slot(int par) { return smem + 8 * kHalf + par * (kHalf / 2); }
+  __device__ __forceinline__ void copy_extra(int par, int step) {
+    step = min(step, n_steps - 1);
+    const uint32_t t = step == n_steps - 1 ? A.tail : 0u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(A.base, A.bytes), (lds_ptr_t)(extra_slot(par) + wave * 1024), 16,
+                                             (int)(A.extra | t), step * (kStep * 2), 0, 0);
   }
 
   // One step in four phases.  PAR: parity of the step's slots.
@@ -229,7 +256,8 @@ struct Product : Tile<A_X, B_X> {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) b0[t][kk] = this->read_b(slot(1, 0, PAR), t, kk);
     this->template copy<A_X, A_G>(A, slot(0, 1, PAR ^ 1), 1, s + 1, ia[PAR ^ 1]);
-    wait_vm<6 + kIdx>();
+    if constexpr (EXTRA) copy_extra(PAR ^ 1, s + 1);
+    wait_vm<6 + kIdx + kMore>();
     barrier();
     this->template quadrant<0, L0>(a0, b0, 0);
     barrier();
@@ -252,10 +280,16 @@ struct Product : Tile<A_X, B_X> {
       a1[i][0] = this->read_a(slot(0, 1, PAR), i, 0);
       a1[i][1] = this->read_a(slot(0, 1, PAR), i, 1);
     }
+    if constexpr (EXTRA) {
+      a2[0] = this->read_a(extra_slot(PAR), 0, 0);
+      a2[1] = this->read_a(extra_slot(PAR), 0, 1);
+    }
     this->template copy<A_X, A_G>(A, slot(0, 0, PAR), 0, s + 2, ia[PAR]);
-    wait_vm<8 + kIdx>();
+    wait_vm<8 + kIdx + kMore>();
     barrier();
     this->template quadrant<1, L1>(a1, b1, 1);
+    if constexpr (EXTRA) this->extra(a2, b1, 1);
+    if constexpr (EXTRA) this->extra(a2, b0, 0);
     barrier();
     // phase 3: most of the next step's A0; quadrant (A1, B0)
 #pragma unroll
@@ -267,7 +301,7 @@ struct Product : Tile<A_X, B_X> {
     if constexpr (B_G) this->load_index(B, s + 3, ib[PAR ^ 1]);
     __builtin_amdgcn_sched_barrier(0);
     this->template copy<B_X, B_G>(B, slot(1, 0, PAR), 0, s + 2, ib[PAR]);
-    wait_vm<8 + kIdx>();
+    wait_vm<8 + kIdx + kMore>();
     barrier();
     this->template quadrant<1, L1>(a1, b0, 0);
     barrier();
@@ -276,6 +310,10 @@ struct Product : Tile<A_X, B_X> {
   __device__ __forceinline__ void run() {
     this->template clear<0, L0>();
     this->template clear<1, L1>();
+    if constexpr (EXTRA) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) this->more[u >> 1][u & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     if (n_steps == 0) return;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -285,13 +323,14 @@ struct Product : Tile<A_X, B_X> {
     this->template copy<A_X, A_G>(A, slot(0, 0, 0), 0, 0, ia[0]);
     this->template copy<B_X, B_G>(B, slot(1, 0, 0), 0, 0, ib[0]);
     this->template copy<A_X, A_G>(A, slot(0, 1, 0), 1, 0, ia[0]);
+    if constexpr (EXTRA) copy_extra(0, 0);
     this->template copy<B_X, B_G>(B, slot(1, 1, 0), 1, 0, ib[0]);
     if constexpr (A_G) this->load_index(A, 2, ia[0]);
     if constexpr (B_G) this->load_index(B, 2, ib[0]);
     __builtin_amdgcn_sched_barrier(0);
     this->template copy<A_X, A_G>(A, slot(0, 0, 1), 0, 1, ia[1]);
     this->template copy<B_X, B_G>(B, slot(1, 0, 1), 0, 1, ib[1]);
-    wait_vm<8>();            // A0 and B0 of step 0
+    wait_vm<8 + kMore>();    // A0 and B0 of step 0
     barrier();
 #pragma unroll
     for (int i = 0; i < (L0 < 3 ? L0 : 3); ++i) {
@@ -423,7 +462,7 @@ struct TileAt {
   int g, row0, m0, m_rows, n0, cols;
 };
 
-template <bool KN, int L0, int L1>
+template <bool KN, int L0, int L1, bool EXTRA = false>
 __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const TileAt& t, uint8_t* smem) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -446,6 +485,13 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
     A.base = a.a_row_index ? base : base + (long long)(t.row0 + t.m0) * a.lda * 2;
     A.bytes = (uint32_t)((a.a_row_index ? a.a_rows : t.m_rows) * a.lda * 2);
     straight_offsets(A, rows, a.lda, chunk, K);
+    A.extra = kOut;
+    if constexpr (EXTRA) {
+      const int r = kTile + 8 * wave + (lane >> 3);
+      if (r < t.m_rows)
+        A.extra = (uint32_t)((a.a_row_index ? (long long)clampi(a.a_row_index[t.row0 + t.m0 + r], 0, a.a_rows - 1) : r) *
+                             a.lda * 2) + chunk * 16;
+    }
   }
   const uint8_t* b = static_cast<const uint8_t*>(a.b) + (long long)t.g * N * K * 2;
   if constexpr (KN) {
@@ -467,39 +513,41 @@ __device__ __forceinline__ void gemm_tile(const moe_gemm_bf16_args& a, const Til
     B.bytes = (uint32_t)t.cols * (uint32_t)K * 2;
     straight_offsets(B, rows, K, chunk, K);
   }
-  typename std::conditional<(L1 > 0), Product<false, KN, false, false, L0, L1>,
+  typename std::conditional<(L1 > 0), Product<false, KN, false, false, L0, L1, EXTRA>,
                             ShortProduct<KN, L0>>::type p(smem, wave, lane, (K + kStep - 1) / kStep, A, B);
   p.run();
 
   // A lane holds 4 consecutive columns of one row in each accumulator; with a
   // straight B its two subtiles make 8 consecutive columns.
   const int wm = wave & 1, wn = wave >> 1, lk = lane >> 4;
+  auto put = [&](int subtile, const f32x4 (&acc)[2][2]) {
+    const int r = (subtile + wm) * 16 + (lane & 15);
+    if (r >= t.m_rows) return;
+    const long long row = t.row0 + t.m0 + r;
+    const float s = a.row_scale ? a.row_scale[row] : 1.0f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const int c = u * 128 + wn * 32 + (KN ? v * 16 + lk * 4 : lk * 8 + v * 4);
+        if (c >= t.cols) continue;
+        const long long at = row * a.ldo + t.n0 + c;
+        const f32x4 x = acc[u][v] * s;
+        if (a.out_dtype == MOE_F32) {
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = x;
+        } else {
+          bf16x4 y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
+          *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at) = y;
+        }
+      }
+  };
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < (h ? L1 : L0); ++i) {
-      const int r = h * 128 + (2 * i + wm) * 16 + (lane & 15);
-      if (r >= t.m_rows) continue;
-      const long long row = t.row0 + t.m0 + r;
-      const float s = a.row_scale ? a.row_scale[row] : 1.0f;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int c = u * 128 + wn * 32 + (KN ? v * 16 + lk * 4 : lk * 8 + v * 4);
-          if (c >= t.cols) continue;
-          const long long at = row * a.ldo + t.n0 + c;
-          const f32x4 x = p.acc[h][i][u][v] * s;
-          if (a.out_dtype == MOE_F32) {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = x;
-          } else {
-            bf16x4 y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (__bf16)x[e];
-            *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.out) + at) = y;
-          }
-        }
-    }
+    for (int i = 0; i < (h ? L1 : L0); ++i) put(h * 8 + 2 * i, p.acc[h][i]);
+  if constexpr (EXTRA) put(16, p.more);
 }
 
 template <bool KN>
@@ -515,6 +563,18 @@ __device__ __forceinline__ int group_rows(const int32_t* offsets, int gi, int G,
   if (gi < 0 || gi >= G) return 0;
   lo = clampi(offsets[gi], 0, total);
   return max(clampi(offsets[gi + 1], 0, total) - lo, 0);
+}
+
+// Row tiles of a group of `rows` rows: its units of kUnit rows are spread
+// evenly over as few tiles of at most kTile + kUnit rows as hold them.  A tile of
+// a few rows takes 0.6 of a full one's time, for it streams the same
+// weights: with tiles of 256 rows and a rest, 32 groups of 4096 x 7168 take 428 us at
+// 256 rows, 726 at 288, 712 at 300 and 1058 at 600; spread evenly 427, 466, 568
+// and 908 (at most 256 rows each: 428, 462, 571, 913, and 851 against 807 at 530).
+__device__ __forceinline__ int units_of(int rows) { return (rows + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int row_tiles_of(int rows) {
+  constexpr int kMost = (kTile + kUnit) / kUnit;
+  return (units_of(rows) + kMost - 1) / kMost;
 }
 
 // Exclusive prefix of v over the workgroup's threads, and the total.
@@ -540,9 +600,9 @@ __device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
   return before;
 }
 
-// The tile list of the large-batch kernel.  A group's rows are cut into tiles of
-// 256 and a rest, in bands of up to kBand row tiles, column tile by column
-// tile, so that tiles which share a weight tile follow one another.  kRun
+// The tile list of the large-batch kernel.  A group's row tiles go in bands of
+// up to kBand, column tile by column tile, so that tiles which share a weight tile
+// follow one another.  kRun
 // consecutive tiles, one round of an XCD's compute units (fewer where that
 // would leave XCDs without any), form a run; run j of
 // the dispatch order belongs to XCD j % 8, and its tiles share a few row and
@@ -554,8 +614,7 @@ __device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
 //
 // The grid is one workgroup per compute unit.  A workgroup's first tile is its
 // own by position; further ones come from its XCD's counter and, when that
-// XCD's runs are all taken, from the next XCD's: tiles differ in time by a
-// factor of two, and workgroups that the hardware hands out one per tile
+// XCD's runs are all taken, from the next XCD's: tiles differ in time, and workgroups that the hardware hands out one per tile
 // leave a tenth of the compute units waiting.
 constexpr int kXcds = 8;
 constexpr int kBand = 4;
@@ -591,7 +650,7 @@ struct TileList {
     int lo, mt[kPer], sum = 0, all;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      mt[i] = i < per ? (group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo) + kTile - 1) / kTile : 0;
+      mt[i] = i < per ? row_tiles_of(group_rows(a.group_offsets, (int)threadIdx.x * per + i, G, a.total_rows, lo)) : 0;
       sum += mt[i];
     }
     int at = prefix(sum, tmp, all);
@@ -640,8 +699,9 @@ struct TileList {
           const uniform_int_t offsets = (uniform_int_t)(uintptr_t)a.group_offsets;
           t.row0 = clampi(offsets[t.g], 0, a.total_rows);
           const int rows = clampi(offsets[t.g + 1], 0, a.total_rows) - t.row0;
-          t.m0 = (band * kBand + rest - n_tile * height) * kTile;
-          t.m_rows = min(rows - t.m0, kTile);
+          const int i = band * kBand + rest - n_tile * height, units = units_of(rows);
+          t.m0 = (int)((long long)units * i / mt) * kUnit;
+          t.m_rows = min(rows, (int)((long long)units * (i + 1) / mt) * kUnit) - t.m0;
           t.n0 = n_tile * kTile;
           t.cols = min(kTile, a.n_out - t.n0);
           return true;
@@ -676,7 +736,8 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(GemmPara
   for (int slot = blockIdx.x / kXcds; list.find(slot, t);) {
     const unsigned popped = list.pop();
     const int l1 = (t.m_rows - 128 + 31) / 32;
-    if (t.m_rows <= 128) short_tile<KN>(p.a, t, smem);
+    if (t.m_rows > kTile) gemm_tile<KN, 4, 4, true>(p.a, t, smem);
+    else if (t.m_rows <= 128) short_tile<KN>(p.a, t, smem);
     else if (l1 > 2) l1 > 3 ? gemm_tile<KN, 4, 4>(p.a, t, smem) : gemm_tile<KN, 4, 3>(p.a, t, smem);
     else l1 > 1 ? gemm_tile<KN, 4, 2>(p.a, t, smem) : gemm_tile<KN, 4, 1>(p.a, t, smem);
     if (!p.next) return;
@@ -903,10 +964,11 @@ int wgrad_splits(int num_groups, int total_rows, int n, int k) {
 long long row_tiles(int num_groups, int total_rows) {
   return (long long)total_rows / kTile + (num_groups < total_rows ? num_groups : total_rows);
 }
-// Up to 64 rows a group on average the weights' stream decides: 64 rows over
-// 33 groups of 4096 x 7168 take 343 us there and 384 with a workgroup per tile;
-// at 124 rows both take 430 to 450, at 182 the stream kernel 547 against 454.
-bool streams_weights(int num_groups, int total_rows) { return total_rows <= 64LL * num_groups; }
+// Up to 48 rows a group on average the weights' stream decides.  32 groups of
+// 4096 x 7168 take, in the stream kernel and in row tiles: at 2 rows a group 307 and
+// 317 us (317 and 323 in the other layout), at 48 328 and 326 (330, 332), at 96
+// 366 and 344 (372, 342), at 160 775 and 374 (787, 358).
+bool streams_weights(int num_groups, int total_rows) { return total_rows <= 48LL * num_groups; }
 // Workgroups of an XCD: one per compute unit (of the whole chip without a device).
 int places() {
   const int cus = cu_count();
@@ -917,7 +979,7 @@ bool valid_dt(moe_dtype_t d) { return d == MOE_BF16 || d == MOE_F32; }
 // element rows that 32-bit byte offsets of a gathered operand can reach
 bool fits31(long long rows, long long ld) { return rows * ld * 2 < (1LL << 31); }
 // a tile's or a step's rows of an operand that is not gathered
-bool tile_fits31(long long ld) { return fits31(kTile, ld); }
+bool tile_fits31(long long ld) { return fits31(kTile + kUnit, ld); }
 
 }  // namespace
 
@@ -939,7 +1001,8 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, vo
     return MOE_ERR_SHAPE;
   if (a.num_groups > kMaxGroups || !valid_dt(a.out_dtype) ||
       (a.b_layout != MOE_B_NK && a.b_layout != MOE_B_KN) ||
-      (long long)a.n_out * a.k_dim * 2 >= (1LL << 31) || !tile_fits31(a.lda))
+      !fits31(a.n_out, a.k_dim) || !tile_fits31(a.lda) ||
+      (a.b_layout == MOE_B_KN && !fits31(kStep, a.n_out)))
     return MOE_ERR_UNSUPPORTED;
   if (a.a_row_index && !fits31(a.a_rows, a.lda)) return MOE_ERR_UNSUPPORTED;
   if (!a.a_row_index && a.a_rows < a.total_rows) return MOE_ERR_SHAPE;

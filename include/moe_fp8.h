@@ -569,8 +569,9 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* args, void* 
  * ordered on one stream.
  * Requires k_dim, n_out, lda, ldo multiples of 8, lda >= k_dim, ldo >= n_out, and
  * a_rows >= total_rows without a_row_index (MOE_ERR_SHAPE); a, b, out 16-byte
- * aligned; 1 <= G <= 1025, n_out * k_dim < 2^30, and with a_row_index
- * a_rows * lda < 2^30 (MOE_ERR_UNSUPPORTED).
+ * aligned; 1 <= G <= 1025, n_out * k_dim < 2^30, n_out < 2^24 with MOE_B_KN,
+ * 288 * lda < 2^30, and with a_row_index a_rows * lda < 2^30
+ * (MOE_ERR_UNSUPPORTED).
  */
 typedef enum { MOE_B_NK = 0, MOE_B_KN = 1 } moe_b_layout_t;
 

@@ -270,6 +270,36 @@ def test_grouped_gemm_bf16(moe, case):
     assert torch.all(o[:, n:] == 5.0)
 
 
+@pytest.mark.parametrize("kn", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("k", [24, 64, 328])
+def test_grouped_gemm_bf16_row_tiles(moe, kn, gather, k):
+    """Groups at the edges of the row tiles (multiples of 32 rows up to 288),
+    each between groups whose rows are not finite."""
+    sizes = []
+    for r in (257, 288, 289, 576, 577, 600, 864, 865, 1153, 161, 287, 32, 33):
+        sizes += [r, 1]
+    off = _offsets(sizes)
+    R, G, n = int(off[-1]), len(sizes), 520
+    rng = np.random.default_rng(k)
+    a, b = _make(rng, (R, k), "bf16"), _make(rng, (G, k, n) if kn else (G, n, k), "bf16", 0.1)
+    poison = off[1:-1:2]                    # the single rows between
+    index = np.arange(R, dtype=np.int32)
+    if gather:
+        index = rng.permutation(R).astype(np.int32)
+    rows = a[0].clone()
+    rows[torch.from_numpy(index[poison].astype(np.int64)).cuda()] = float("nan")
+    log(f"moe_grouped_gemm_bf16 row tiles, kn {kn}, gather {gather}, k {k}")
+    got = moe.moe_grouped_gemm_bf16(rows, b[0], to_dev(off), R, b_kn=kn,
+                                    a_row_index=to_dev(index) if gather else None,
+                                    out_dtype=torch.float32)
+    want, mag = train.grouped_gemm(a[1], b[1], off, index if gather else None, None, kn)
+    ok = np.setdiff1d(np.arange(R), poison)
+    at = torch.from_numpy(ok).cuda()
+    _close(got[at], want[ok], UB["f32"] * np.abs(want[ok]) + (k + 8) * 2.0 ** -23 * mag[ok], "out")
+    assert torch.isnan(got[torch.from_numpy(poison.astype(np.int64)).cuda()]).all()
+
+
 def test_grouped_gemm_bf16_keeps_non_finite_rows_apart(moe):
     rng = np.random.default_rng(8)
     sizes = [5, 130, 0, 9]

@@ -82,6 +82,13 @@ def test_grouped_gemm_arguments(lib, change, status):
     assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **change), None, 0, None) == status
 
 
+@pytest.mark.parametrize("change,status", [
+    (dict(b_layout=1, n_out=1 << 24, ldo=1 << 24), 6),      # a step's rows of B pass 32 bits
+    (dict(lda=1 << 22), 6), (dict(n_out=1 << 26, ldo=1 << 26, total_rows=0), 6)])
+def test_grouped_gemm_refuses_sizes_past_its_offsets(lib, change, status):
+    assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **change), None, 0, None) == status
+
+
 def test_grouped_gemm_workspace(lib):
     need = lib.moe_grouped_gemm_bf16_workspace_bytes
     assert need(33, 144, 4096, 7168) == 0           # few rows a group: the weights' stream
