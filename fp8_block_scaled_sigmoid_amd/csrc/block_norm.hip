@@ -13,6 +13,11 @@
 //   over what the gate is shared by)
 // Both statistics come from the rows themselves, so nothing but r and b has to
 // be kept between the passes.
+//
+// Memory bounds both passes (forward x, b, r, h; backward r, dr, b, dh, dx, db).
+// At 8192 x 7168 in bf16: forward 470 MB in 93 us, 5.05 TB/s; backward 705 MB in
+// 152 us + 5 us for the sums over tokens, 4.5 TB/s (a large copy: 4.78).  At one
+// token the forward kernel takes 4.4 us: launch, the row's latency, two sums.
 #include <type_traits>
 
 #include "rows.h"
@@ -27,7 +32,13 @@ constexpr int kFwdWaves = 8, kBwdWaves = 16;      // waves of a workgroup
 
 // How rows are laid over threads: `wpr` waves share a row, a workgroup holds
 // `groups` rows at a time, and a thread owns vectors t, t + 64 wpr, ... of its
-// row, `items` of them.
+// row, `items` of them.  Forward workgroups have 8 waves, the backward ones 16: a
+// forward row has one reduction after another and more, smaller workgroups on a
+// compute unit hide it (93 us at 8192 x 7168, against 97 with 16 waves
+// and 100 with 4); a
+// backward workgroup keeps two float sums for each channel, and the more
+// waves share a row the more registers are left for the next row's loads.
+// Widths up to 512 run one wave per row, without barriers.
 struct RowShape {
   int wpr, groups, items;
 };
@@ -180,8 +191,12 @@ __global__ __launch_bounds__(kFwdWaves * 64) void block_norm_kernel(FwdParams p)
 // Two sums serve all three gradients: dw_pre, and S = sum_t d b^ times a
 // per-row gate, from which dw_post = beta gate_c S and, for a gate per channel,
 // dgate = beta w_post S.  A row's four inputs are read once, the next row's
-// while one is worked on; rows wider than 8192 do not fit the registers, and
-// read theirs again after the first reduction instead (from L2).
+// while one is worked on (202 -> 159 us at 8192 x 7168, with the sums by DPP);
+// a gate for each element has no registers left for that (1021 x 2049 in
+// float: 18 us, of which two rows' latency is most).  Rows wider than 8192 do not fit
+// the registers, and read theirs again after the first reduction instead
+// (from L2).  One workgroup per compute unit: 256 partial sums of each channel,
+// 15 MB at 7168, which the second kernel adds in 5 us.
 struct BwdParams {
   moe_block_norm_bwd_args a;
   int wpr, groups;
