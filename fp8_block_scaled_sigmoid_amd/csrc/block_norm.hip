@@ -29,6 +29,7 @@ using namespace moe;
 constexpr int kMaxWaves = 16;
 constexpr int kMaxWidth = 16384;
 constexpr int kFwdWaves = 8, kBwdWaves = 16;      // waves of a workgroup
+constexpr int kMaxBlocks = 1 << 20, kMaxRows = 1 << 30;
 
 // How rows are laid over threads: `wpr` waves share a row, a workgroup holds
 // `groups` rows at a time, and a thread owns vectors t, t + 64 wpr, ... of its
@@ -456,8 +457,8 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_args* args, hipStrea
   if (!args) return MOE_ERR_NULL;
   const moe_block_norm_args& a = *args;
   if (a.T < 0 || a.H < 1 || a.H > kMaxWidth || !(a.eps > 0.0f)) return MOE_ERR_SHAPE;
-  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) || a.gate_mode < MOE_GATE_NONE ||
-      a.gate_mode > MOE_GATE_FULL)
+  if (a.T > kMaxRows || !valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) ||
+      a.gate_mode < MOE_GATE_NONE || a.gate_mode > MOE_GATE_FULL)
     return MOE_ERR_UNSUPPORTED;
   if (bad_ld(a.x, a.ldx, a.H) || bad_ld(a.b, a.ldb, a.H) || bad_ld(a.h, a.ldh, a.H) ||
       (a.b && bad_ld(a.r, a.ldr, a.H)) ||
@@ -476,7 +477,8 @@ extern "C" moe_status_t moe_block_norm(const moe_block_norm_args* args, hipStrea
   const RowShape s = row_shape(a.H, kFwdWaves);
   FwdParams p{a, s.wpr, s.groups};
   if (!a.b) p.a.gate_mode = MOE_GATE_NONE;
-  const int blocks = (a.T + s.groups - 1) / s.groups;
+  // a launch holds less than 2^32 threads; longer batches go round the kernel's loop
+  const int need = (a.T - 1) / s.groups + 1, blocks = need < kMaxBlocks ? need : kMaxBlocks;
   with_types(a.x_dtype, a.b_dtype, s.items, [&](auto x, auto b, auto items) {
     using X = typename decltype(x)::type;
     using B = typename decltype(b)::type;
@@ -496,8 +498,8 @@ extern "C" moe_status_t moe_block_norm_backward(const moe_block_norm_bwd_args* a
   if (!args) return MOE_ERR_NULL;
   const moe_block_norm_bwd_args& a = *args;
   if (a.T < 0 || a.H < 1 || a.H > kMaxWidth || !(a.eps > 0.0f)) return MOE_ERR_SHAPE;
-  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) || a.gate_mode < MOE_GATE_NONE ||
-      a.gate_mode > MOE_GATE_FULL)
+  if (a.T > kMaxRows || !valid_dtype(a.x_dtype) || !valid_dtype(a.b_dtype) ||
+      a.gate_mode < MOE_GATE_NONE || a.gate_mode > MOE_GATE_FULL)
     return MOE_ERR_UNSUPPORTED;
   const bool full = a.gate_mode == MOE_GATE_FULL;
   if (bad_ld(a.r, a.ldr, a.H) || bad_ld(a.dr, a.lddr, a.H) || bad_ld(a.dh, a.lddh, a.H) ||

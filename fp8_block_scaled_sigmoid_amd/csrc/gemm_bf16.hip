@@ -751,14 +751,13 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_kernel(GemmPara
 // line) where a weight row is cut at a unit's edge; workgroup b takes units
 // [U b / blocks, U (b + 1) / blocks), in pieces of at most 256 columns and
 // about equal width inside one group.
-
 template <bool KN>
 __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(GemmParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const moe_gemm_bf16_args& a = p.a;
   int* tmp = reinterpret_cast<int*>(smem);
-  constexpr int kUnit = KN ? 64 : 16;
-  const int G = a.num_groups, units = (a.n_out + kUnit - 1) / kUnit;
+  constexpr int kPiece = KN ? 64 : 16;
+  const int G = a.num_groups, units = (a.n_out + kPiece - 1) / kPiece;
   const int per = (G + kThreads - 1) / kThreads;
   int sum = 0, lo;
 #pragma unroll
@@ -797,10 +796,10 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_bf16_stream_kernel(G
     t.m0 = m * 128;
     t.m_rows = min(rows - t.m0, 128);
     const int here = (int)min((long long)(units - u), left);      // units of this row tile
-    const int pieces = (here + kTile / kUnit - 1) / (kTile / kUnit);
+    const int pieces = (here + kTile / kPiece - 1) / (kTile / kPiece);
     const int take = (here + pieces - 1) / pieces;
-    t.n0 = u * kUnit;
-    t.cols = min(take * kUnit, a.n_out - t.n0);
+    t.n0 = u * kPiece;
+    t.cols = min(take * kPiece, a.n_out - t.n0);
     __syncthreads();              // LDS is free again
     short_tile<KN>(a, t, smem);
     left -= take;

@@ -149,13 +149,21 @@ extern "C" moe_status_t moe_swiglu_backward(const void* a, const void* dh, moe_d
       !element_aligned(dgate, MOE_F32))
     return MOE_ERR_ALIGN;
   if (moe_status_t s = check_device()) return s;
-  const BwdParams p{a, dh, row_gate, da, hg, dgate, lda, lddh, ldda, ldhg, R, I,
-                    waves_of_row(I)};
-  const int rows = 4 / p.wpr;
-  const dim3 grid((unsigned)((R + (long long)rows - 1) / rows));
-  if (dt == MOE_BF16)
-    hipLaunchKernelGGL(swiglu_bwd_kernel<bf16_t>, grid, dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL(swiglu_bwd_kernel<float>, grid, dim3(256), 0, stream, p);
-  return launch_status();
+  const int wpr = waves_of_row(I), rows = 4 / wpr;
+  const long long esize = dt == MOE_BF16 ? 2 : 4;
+  auto at = [](const void* p, long long bytes) -> const void* { return p ? static_cast<const char*>(p) + bytes : p; };
+  const int slab = rows << 22;            // a launch holds less than 2^32 threads
+  for (long long r0 = 0; r0 < R; r0 += slab) {
+    const int n = (int)(R - r0 < slab ? R - r0 : slab);
+    const BwdParams p{at(a, r0 * lda * esize), at(dh, r0 * lddh * esize), row_gate ? row_gate + r0 : nullptr,
+                      const_cast<void*>(at(da, r0 * ldda * esize)), const_cast<void*>(at(hg, r0 * ldhg * esize)),
+                      dgate ? dgate + r0 : nullptr, lda, lddh, ldda, ldhg, n, I, wpr};
+    const dim3 grid((unsigned)((n - 1) / rows + 1));
+    if (dt == MOE_BF16)
+      hipLaunchKernelGGL(swiglu_bwd_kernel<bf16_t>, grid, dim3(256), 0, stream, p);
+    else
+      hipLaunchKernelGGL(swiglu_bwd_kernel<float>, grid, dim3(256), 0, stream, p);
+    if (moe_status_t s = launch_status()) return s;
+  }
+  return MOE_OK;
 }

@@ -495,7 +495,8 @@ typedef enum {
  * w_post float [H].  Row strides (ld*, in elements) are at least H and free
  * otherwise; pointers need the alignment of their element type only.  r may
  * be x and h may be b (the same pointer and stride).
- * Requires 1 <= H <= 16384, eps > 0 (MOE_ERR_SHAPE).
+ * Requires 1 <= H <= 16384, eps > 0 (MOE_ERR_SHAPE), T <= 2^30
+ * (MOE_ERR_UNSUPPORTED).
  */
 typedef struct {
   int T, H;

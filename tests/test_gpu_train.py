@@ -591,6 +591,31 @@ def test_refusals(moe):
         moe.moe_grad_clip(moe.GradList([bf(4)]), -1.0)
 
 
+@pytest.mark.parametrize("H,T", [(8, (8 << 20) + 5), (2056, (1 << 20) + 7)])
+def test_block_norm_more_rows_than_a_launch_holds(moe, H, T):
+    """Rows past the first round of the grid: the same bits as in a small call."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.empty(T, H, device="cuda", dtype=torch.bfloat16).normal_(generator=gen)
+    w = torch.empty(H, device="cuda").normal_(generator=gen)
+    log(f"moe_block_norm {T} x {H}")
+    h = moe.moe_block_norm(x, w_pre=w)[1]
+    for rows in (slice(0, 9), slice(T - 300, T)):
+        assert torch.equal(h[rows], moe.moe_block_norm(x[rows], w_pre=w)[1])
+
+
+def test_swiglu_backward_more_rows_than_a_launch_holds(moe):
+    R, I = (16 << 20) + 11, 8
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    a = torch.empty(R, 2 * I, device="cuda", dtype=torch.bfloat16).normal_(generator=gen)
+    dh = torch.empty(R, I, device="cuda", dtype=torch.bfloat16).normal_(generator=gen)
+    g = torch.rand(R, device="cuda", generator=gen)
+    log(f"moe_swiglu_backward {R} x {I}")
+    got = moe.moe_swiglu_backward(a, dh, g)
+    for rows in (slice(0, 9), slice(R - 300, R)):
+        for x, y in zip(got, moe.moe_swiglu_backward(a[rows], dh[rows], g[rows])):
+            assert torch.equal(x[rows], y)
+
+
 def test_on_another_stream(moe):
     rng = np.random.default_rng(15)
     x, b = _make(rng, (64, 512), "bf16")[0], _make(rng, (64, 512), "bf16")[0]

@@ -82,6 +82,12 @@ def test_grouped_gemm_arguments(lib, change, status):
     assert lib.moe_grouped_gemm_bf16(_args(moe.GemmBf16Args, GEMM, **change), None, 0, None) == status
 
 
+def test_block_norm_refuses_more_rows_than_its_counters_hold(lib):
+    assert lib.moe_block_norm(_args(moe.BlockNormArgs, NORM, T=(1 << 30) + 1), None) == 6
+    assert lib.moe_block_norm_backward(_args(moe.BlockNormBwdArgs, BWD, T=(1 << 30) + 1), None, 0,
+                                       None) == 6
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(b_layout=1, n_out=1 << 24, ldo=1 << 24), 6),      # a step's rows of B pass 32 bits
     (dict(lda=1 << 22), 6), (dict(n_out=1 << 26, ldo=1 << 26, total_rows=0), 6)])
