@@ -610,20 +610,22 @@ __device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
 
 // The tile list of the large-batch kernel.  A group's row tiles go in bands of
 // up to kBand, column tile by column tile, so that tiles which share a weight tile
-// follow one another.  kRun
-// consecutive tiles, one round of an XCD's compute units (fewer where that
-// would leave XCDs without any), form a run; run j of
+// follow one another.  kRun consecutive tiles, one round of an XCD's compute
+// units (fewer where that would leave XCDs without any), form a run; run j of
 // the dispatch order belongs to XCD j % 8, and its tiles share a few row and
 // column tiles through that XCD's L2.  Runs are dispatched in the order of a
-// golden-ratio stride over the list, not in list order: a group with many
-// rows needs the matrix cores and hardly any memory, one with few rows the
-// reverse, and this way every moment has some of both (in list order the
-// groups' weights arrive at the memory's rate while the matrix cores wait).
+// golden-ratio stride over the list: a group with many rows needs the matrix
+// cores and hardly any memory, one with few rows the reverse, and this way
+// every moment has some of both (33 groups of together 16384 rows, even and
+// uneven: 810 and 871 us, in list order 812 and 884).  Runs of 16, 32 and 64 tiles
+// take 858, 852 and 840 us and 935, 910 and 909; bands of 2, 4 and 8 row tiles 840,
+// 852 and 853, and 923, 910 and 917 (on a card whose clock was lower).
 //
 // The grid is one workgroup per compute unit.  A workgroup's first tile is its
 // own by position; further ones come from its XCD's counter and, when that
-// XCD's runs are all taken, from the next XCD's: tiles differ in time, and workgroups that the hardware hands out one per tile
-// leave a tenth of the compute units waiting.
+// XCD's runs are all taken, from the next XCD's: tiles differ in time, and
+// workgroups that the hardware hands out one per tile leave a tenth of the
+// compute units waiting.
 constexpr int kXcds = 8;
 constexpr int kBand = 4;
 constexpr int kRun = 32;

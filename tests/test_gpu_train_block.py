@@ -85,6 +85,36 @@ def test_block_gradients(stream):
     assert abs(after - 0.1) <= 1e-5
 
 
+def test_block_one_token():
+    """One token: nearly every expert has no rows, and its gradient is zero."""
+    from fp8_block_scaled_sigmoid_amd.train import BlockWeights, MoEBlock
+    H, I, N, k = 256, 64, 32, 2
+    gen = torch.Generator(device="cuda").manual_seed(6)
+
+    def normal(*shape, std=1.0, dtype=torch.float32):
+        return torch.empty(*shape, device="cuda").normal_(0, std, generator=gen).to(dtype)
+
+    bf = torch.bfloat16
+    w = BlockWeights(normal(N, H, std=0.3, dtype=bf), normal(N, std=0.05),
+                     normal(N + 1, 2 * I, H, std=0.15, dtype=bf), normal(N + 1, H, I, std=0.2, dtype=bf),
+                     1 + normal(H, std=0.1), 1 + normal(H, std=0.1), normal(H))
+    x, dr, dh_next = normal(1, H), normal(1, H), normal(1, H, dtype=bf)
+    next_w = 1 + normal(H, std=0.1)
+    block = MoEBlock(w, k)
+    log("MoEBlock forward and backward, one token")
+    r, h_next, saved = block.forward(x, next_w_pre=next_w)
+    dx, dw_next = block.backward(saved, dr, dh_next, next_w)
+    idx = saved[2].long().cpu()
+    rr, hr, want = _reference(w, x, idx, k, 1.0, 1.0, block.eps, dr, next_w, dh_next)
+    got = {"r": r, "h_next": h_next, "x": dx, "next": dw_next, **block.grads}
+    for name, ref in {"r": rr, "h_next": hr, **want}.items():
+        err = float((got[name].double().cpu() - ref).norm() / ref.norm())
+        print(f"{name}: relative L2 error {err:.2e}")
+        assert err <= BAR, name
+    unused = [e for e in range(N) if e not in idx[0].tolist()]
+    assert torch.all(block.grads["w1"][unused] == 0) and torch.all(block.grads["w2"][unused] == 0)
+
+
 def test_training_example():
     sys.path.insert(0, os.path.join(ROOT, "examples"))
     try:
