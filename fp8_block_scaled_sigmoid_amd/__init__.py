@@ -195,6 +195,20 @@ def _dev(t, dtype, name):
     return t
 
 
+def _empty(stream, *shape, dtype, device, zeros=False):
+    """Memory of a call on `stream` (None: the current one).  It belongs to
+    that stream: the allocator gives it to later work of that stream only, also
+    where the call drops it with its kernels still to run.  The caller's stream
+    is noted as well, where the caller will read and drop a result."""
+    make = torch.zeros if zeros else torch.empty
+    if stream is None:
+        return make(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(*shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 # ---------------------------------------------------------------------------
 # the C entry points
 
@@ -215,14 +229,14 @@ def moe_route_topk(x, w_router, bias, k, scores=True, idx=None, gate=None, ws=No
     _dev(x, torch.bfloat16, "x"), _dev(w_router, torch.bfloat16, "w_router")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = torch.empty(T, N, dtype=torch.float32, device=x.device)
+        scores = _empty(stream, T, N, dtype=torch.float32, device=x.device)
     elif scores is False:
         scores = None
-    idx = torch.empty(T, k, dtype=torch.int32, device=x.device) if idx is None else idx
-    gate = torch.empty(T, k, dtype=torch.float32, device=x.device) if gate is None else gate
+    idx = _empty(stream, T, k, dtype=torch.int32, device=x.device) if idx is None else idx
+    gate = _empty(stream, T, k, dtype=torch.float32, device=x.device) if gate is None else gate
     if ws is None:
-        ws = torch.empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                         device=x.device)
+        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                    device=x.device)
     _check("moe_route_topk", lib().moe_route_topk(_ptr(x), _ptr(w_router), _ptr(bias), T, H, N, k,
                                                   n_groups, topk_groups, _ptr(scores), _ptr(idx),
                                                   _ptr(gate), _ptr(ws), ws.numel(), _stream(stream)))
@@ -239,17 +253,17 @@ def moe_route_topk_quant_x(x, w_router, bias, k, x_q=None, x_d=None, scores=True
     _dev(x, torch.bfloat16, "x"), _dev(w_router, torch.bfloat16, "w_router")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = torch.empty(T, N, dtype=torch.float32, device=x.device)
+        scores = _empty(stream, T, N, dtype=torch.float32, device=x.device)
     elif scores is False:
         scores = None
-    idx = torch.empty(T, k, dtype=torch.int32, device=x.device) if idx is None else idx
-    gate = torch.empty(T, k, dtype=torch.float32, device=x.device) if gate is None else gate
-    x_q = torch.empty(T, H, dtype=torch.uint8, device=x.device) if x_q is None else x_q
-    x_d = torch.empty(T, H // 128, dtype=torch.float32, device=x.device) if x_d is None else x_d
+    idx = _empty(stream, T, k, dtype=torch.int32, device=x.device) if idx is None else idx
+    gate = _empty(stream, T, k, dtype=torch.float32, device=x.device) if gate is None else gate
+    x_q = _empty(stream, T, H, dtype=torch.uint8, device=x.device) if x_q is None else x_q
+    x_d = _empty(stream, T, H // 128, dtype=torch.float32, device=x.device) if x_d is None else x_d
     _dev(x_q, torch.uint8, "x_q"), _dev(x_d, torch.float32, "x_d")
     if ws is None:
-        ws = torch.empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                         device=x.device)
+        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                    device=x.device)
     _check("moe_route_topk_quant_x",
            lib().moe_route_topk_quant_x(_ptr(x), _ptr(w_router), _ptr(bias), T, H, N, k, n_groups,
                                         topk_groups, _ptr(scores), _ptr(idx), _ptr(gate),
@@ -270,14 +284,14 @@ def moe_route_topk_fp8(x_q, x_d, w_router_q, w_router_d, bias, k, scores=True, i
     _dev(w_router_q, torch.uint8, "w_router_q"), _dev(w_router_d, torch.float32, "w_router_d")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = torch.empty(T, N, dtype=torch.float32, device=x_q.device)
+        scores = _empty(stream, T, N, dtype=torch.float32, device=x_q.device)
     elif scores is False:
         scores = None
-    idx = torch.empty(T, k, dtype=torch.int32, device=x_q.device) if idx is None else idx
-    gate = torch.empty(T, k, dtype=torch.float32, device=x_q.device) if gate is None else gate
+    idx = _empty(stream, T, k, dtype=torch.int32, device=x_q.device) if idx is None else idx
+    gate = _empty(stream, T, k, dtype=torch.float32, device=x_q.device) if gate is None else gate
     if ws is None:
-        ws = torch.empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                         device=x_q.device)
+        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                    device=x_q.device)
     _check("moe_route_topk_fp8",
            lib().moe_route_topk_fp8(_ptr(x_q), _ptr(x_d), _ptr(w_router_q), _ptr(w_router_d),
                                     _ptr(bias), T, H, N, k, n_groups, topk_groups, _ptr(scores),
@@ -290,8 +304,8 @@ def moe_topk_from_scores(scores, bias, k, idx=None, gate=None, n_groups=1, topk_
                          stream=None):
     T, N = scores.shape
     _dev(scores, torch.float32, "scores"), _dev(bias, torch.float32, "bias")
-    idx = torch.empty(T, k, dtype=torch.int32, device=scores.device) if idx is None else idx
-    gate = torch.empty(T, k, dtype=torch.float32, device=scores.device) if gate is None else gate
+    idx = _empty(stream, T, k, dtype=torch.int32, device=scores.device) if idx is None else idx
+    gate = _empty(stream, T, k, dtype=torch.float32, device=scores.device) if gate is None else gate
     _check("moe_topk_from_scores", lib().moe_topk_from_scores(
         _ptr(scores), _ptr(bias), T, N, k, n_groups, topk_groups, _ptr(idx), _ptr(gate),
         _stream(stream)))
@@ -310,14 +324,14 @@ def moe_permute(idx, N, with_shared=True, out=None, ws=None, stream=None):
     dev = idx.device
     if out is None:
         R = T * k + (T if with_shared else 0)
-        out = (torch.empty(N, dtype=torch.int32, device=dev),
-               torch.empty(N + 2, dtype=torch.int32, device=dev),
-               torch.empty(T, k, dtype=torch.int32, device=dev),
-               torch.empty(R, dtype=torch.int32, device=dev))
+        out = (_empty(stream, N, dtype=torch.int32, device=dev),
+               _empty(stream, N + 2, dtype=torch.int32, device=dev),
+               _empty(stream, T, k, dtype=torch.int32, device=dev),
+               _empty(stream, R, dtype=torch.int32, device=dev))
     counts, offsets, row_of, token_of = out
     nbytes = moe_permute_workspace_bytes(T, N, k)
     if ws is None:
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        ws = _empty(stream, max(nbytes, 16), dtype=torch.uint8, device=dev)
     _check("moe_permute", lib().moe_permute(_ptr(idx), T, N, k, 1 if with_shared else 0,
                                             _ptr(counts), _ptr(offsets), _ptr(row_of),
                                             _ptr(token_of), _ptr(ws), ws.numel(),
@@ -348,8 +362,8 @@ def fp8_quant_1x128(x, q=None, d=None, stream=None):
     dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[x.dtype]
     if x.stride(1) != 1:
         raise ValueError("x: rows must be contiguous")
-    q = torch.empty(rows, cols, dtype=torch.uint8, device=x.device) if q is None else q
-    d = torch.empty(rows, cols // 128, dtype=torch.float32, device=x.device) if d is None else d
+    q = _empty(stream, rows, cols, dtype=torch.uint8, device=x.device) if q is None else q
+    d = _empty(stream, rows, cols // 128, dtype=torch.float32, device=x.device) if d is None else d
     _check("fp8_quant_1x128", lib().fp8_quant_1x128(_ptr(x), dt, rows, cols, x.stride(0), _ptr(q),
                                                     _ptr(d), _stream(stream)))
     return q, d
@@ -361,8 +375,8 @@ def fp8_quant_128x128(w, interleave_gate_up=False, q=None, d=None, stream=None):
         w = w.unsqueeze(0)
     B, rows, cols = w.shape
     _dev(w, torch.bfloat16, "w")
-    q = torch.empty(B, rows, cols, dtype=torch.uint8, device=w.device) if q is None else q
-    d = torch.empty(B, rows // 128, cols // 128, dtype=torch.float32, device=w.device) \
+    q = _empty(stream, B, rows, cols, dtype=torch.uint8, device=w.device) if q is None else q
+    d = _empty(stream, B, rows // 128, cols // 128, dtype=torch.float32, device=w.device) \
         if d is None else d
     _check("fp8_quant_128x128", lib().fp8_quant_128x128(_ptr(w), B, rows, cols,
                                                         1 if interleave_gate_up else 0, _ptr(q),
@@ -380,12 +394,12 @@ def moe_grouped_gemm_fp8(a_q, a_d, b_q, b_d, group_offsets, total_rows, epilogue
     dev = a_q.device
     if out is None:
         if epilogue == MOE_EPI_SWIGLU_FP8:
-            out = torch.empty(total_rows, n_out // 2, dtype=torch.uint8, device=dev)
-            out_d = torch.empty(total_rows, n_out // 256, dtype=torch.float32, device=dev)
+            out = _empty(stream, total_rows, n_out // 2, dtype=torch.uint8, device=dev)
+            out_d = _empty(stream, total_rows, n_out // 256, dtype=torch.float32, device=dev)
         elif epilogue == MOE_EPI_BF16:
-            out = torch.empty(total_rows, n_out, dtype=torch.bfloat16, device=dev)
+            out = _empty(stream, total_rows, n_out, dtype=torch.bfloat16, device=dev)
         else:
-            out = torch.empty(total_rows, n_out, dtype=torch.float32, device=dev)
+            out = _empty(stream, total_rows, n_out, dtype=torch.float32, device=dev)
     args = GemmArgs(a_q.data_ptr(), a_d.data_ptr(), a_q.stride(0), a_q.shape[0],
                     a_row_index.data_ptr() if a_row_index is not None else None,
                     b_q.data_ptr(), b_d.data_ptr(), group_offsets.data_ptr(), G, total_rows,
@@ -409,8 +423,8 @@ def fp8_transpose_128x128(w_q, w_d, wt_q=None, wt_d=None, stream=None):
     B, rows, cols = w_q.shape
     _dev(w_q, torch.uint8, "w_q"), _dev(w_d, torch.float32, "w_d")
     dev = w_q.device
-    wt_q = torch.empty(B, cols, rows, dtype=torch.uint8, device=dev) if wt_q is None else wt_q
-    wt_d = torch.empty(B, cols // 128, rows // 128, dtype=torch.float32, device=dev) \
+    wt_q = _empty(stream, B, cols, rows, dtype=torch.uint8, device=dev) if wt_q is None else wt_q
+    wt_d = _empty(stream, B, cols // 128, rows // 128, dtype=torch.float32, device=dev) \
         if wt_d is None else wt_d
     _check("fp8_transpose_128x128", lib().fp8_transpose_128x128(
         _ptr(w_q), _ptr(w_d), B, rows, cols, _ptr(wt_q), _ptr(wt_d), _stream(stream)))
@@ -436,9 +450,10 @@ def fp8_quant_tokens_128(x, group_offsets, ldt=None, xt_q=None, xt_d=None, pad_o
     _dev(group_offsets, torch.int32, "group_offsets")
     ldt = tokens_padded_width(rows, G) if ldt is None else ldt
     dev = x.device
-    xt_q = torch.empty(cols, ldt, dtype=torch.uint8, device=dev) if xt_q is None else xt_q
-    xt_d = torch.empty(cols, ldt // 128, dtype=torch.float32, device=dev) if xt_d is None else xt_d
-    pad_offsets = torch.empty(G + 1, dtype=torch.int32, device=dev) if pad_offsets is None \
+    xt_q = _empty(stream, cols, ldt, dtype=torch.uint8, device=dev) if xt_q is None else xt_q
+    xt_d = _empty(stream, cols, ldt // 128, dtype=torch.float32, device=dev) \
+        if xt_d is None else xt_d
+    pad_offsets = _empty(stream, G + 1, dtype=torch.int32, device=dev) if pad_offsets is None \
         else pad_offsets
     _check("fp8_quant_tokens_128", lib().fp8_quant_tokens_128(
         _ptr(x), dt, rows, cols, x.stride(0), _ptr(group_offsets), G, _ptr(xt_q), _ptr(xt_d),
@@ -456,7 +471,7 @@ def moe_grouped_wgrad_fp8(a_q, a_d, b_q, b_d, pad_offsets, out=None, stream=None
                      (b_q, torch.uint8, "b_q"), (b_d, torch.float32, "b_d"),
                      (pad_offsets, torch.int32, "pad_offsets")):
         _dev(t, dt, n)
-    out = torch.empty(G, N, K, dtype=torch.float32, device=a_q.device) if out is None else out
+    out = _empty(stream, G, N, K, dtype=torch.float32, device=a_q.device) if out is None else out
     _check("moe_grouped_wgrad_fp8", lib().moe_grouped_wgrad_fp8(
         _ptr(a_q), _ptr(a_d), lda, N, _ptr(b_q), _ptr(b_d), ldb, K, _ptr(pad_offsets), G,
         _ptr(out), _stream(stream)))
@@ -478,7 +493,7 @@ def moe_grouped_dgrad_fp8(dy, wt_q, wt_d, group_offsets, epilogue=MOE_EPI_BF16, 
 def moe_combine(out_rows, gate, row_of, shared_row0, residual=None, y=None, stream=None):
     T, k = row_of.shape
     H = out_rows.shape[1]
-    y = torch.empty(T, H, dtype=torch.bfloat16, device=out_rows.device) if y is None else y
+    y = _empty(stream, T, H, dtype=torch.bfloat16, device=out_rows.device) if y is None else y
     _check("moe_combine", lib().moe_combine(_ptr(out_rows), _ptr(gate), _ptr(row_of), shared_row0,
                                             T, H, k, _ptr(residual), _ptr(y), _stream(stream)))
     return y
@@ -498,7 +513,8 @@ def moe_seq_balance_loss(idx, gate, seq_offsets, n_experts, alpha=1e-4, loss=Non
     _dev(idx, torch.int32, "idx"), _dev(gate, torch.float32, "gate")
     _dev(seq_offsets, torch.int32, "seq_offsets")
     S = seq_offsets.numel() - 1
-    loss = torch.empty(max(S, 0), dtype=torch.float32, device=idx.device) if loss is None else loss
+    loss = _empty(stream, max(S, 0), dtype=torch.float32, device=idx.device) \
+        if loss is None else loss
     _check("moe_seq_balance_loss", lib().moe_seq_balance_loss(
         _ptr(idx), _ptr(gate), _ptr(seq_offsets), S, T, n_experts, k, alpha, _ptr(loss),
         _stream(stream)))
@@ -510,7 +526,7 @@ def moe_probe_fp8_mfma(blocks, iters, sink=None, stream=None):
     blocks * 4 waves, each issuing iters * 16 16x16x128 FP8 MFMAs.  Returns
     (sink, flops)."""
     if sink is None:
-        sink = torch.empty(blocks * 256, dtype=torch.float32, device="cuda")
+        sink = _empty(stream, blocks * 256, dtype=torch.float32, device="cuda")
     _check("moe_probe_fp8_mfma", lib().moe_probe_fp8_mfma(blocks, iters, _ptr(sink),
                                                           _stream(stream)))
     return sink, float(blocks) * 4 * iters * 16 * 65536
@@ -522,7 +538,7 @@ def moe_probe_hbm(mode, buf, sink=None, stream=None):
     loads in flight per lane; ordinary, four), modes 1 and 3 write them
     (non-temporal; ordinary stores).  Returns the sink (read modes) or None."""
     if mode in (0, 2) and sink is None:
-        sink = torch.zeros(1, dtype=torch.int32, device=buf.device)
+        sink = _empty(stream, 1, dtype=torch.int32, device=buf.device, zeros=True)
     _check("moe_probe_hbm", lib().moe_probe_hbm(mode, _ptr(buf), buf.numel() * buf.element_size(),
                                                 _ptr(sink), _stream(stream)))
     return sink
@@ -544,10 +560,10 @@ def moe_layer_forward(w, x, k, gamma=1e-3, n_groups=1, topk_groups=1, router_fp8
     with_shared = w.G == w.N + 1
     if router_fp8 and w.w_router_q is None:
         raise ValueError("router_fp8 needs MoEWeights(..., router_fp8=True)")
-    y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _empty(stream, T, H, dtype=torch.bfloat16, device=x.device) if y is None else y
     if ws is None:
-        ws = torch.empty(max(moe_layer_workspace_bytes(T, H, w.N, k, w.I, with_shared), 256),
-                         dtype=torch.uint8, device=x.device)
+        ws = _empty(stream, max(moe_layer_workspace_bytes(T, H, w.N, k, w.I, with_shared), 256),
+                    dtype=torch.uint8, device=x.device)
     a = LayerArgs(x.data_ptr(), w.w_router.data_ptr(),
                   w.w_router_q.data_ptr() if w.w_router_q is not None else None,
                   w.w_router_d.data_ptr() if w.w_router_d is not None else None,
@@ -627,14 +643,14 @@ def moe_block_norm(x, b=None, w_pre=None, w_post=None, gate=None, alpha=1.0, bet
     if b is not None:
         bt = b.dtype
         _dtype_code(b, "b")
-        r = torch.empty(T, H, dtype=x.dtype, device=x.device) if r is None else r
+        r = _empty(stream, T, H, dtype=x.dtype, device=x.device) if r is None else r
     else:
         if gate is not None or w_post is not None:
             raise ValueError("gate and w_post belong to a block output b")
         bt = h.dtype if h is not None else x.dtype
         r = None
     if h is None and w_pre is not None:
-        h = torch.empty(T, H, dtype=bt, device=x.device)
+        h = _empty(stream, T, H, dtype=bt, device=x.device)
     mode, gp, ldg = _gate(gate, T, H, bt)
     a = BlockNormArgs(T, H, xdt, _DT.get(bt, -1), *_rows(x, T, H, x.dtype, "x"),
                       *_rows(b, T, H, bt, "b"), _vector(w_pre, H, "w_pre"),
@@ -660,24 +676,24 @@ def moe_block_norm_backward(r, dr=None, dh=None, b=None, w_pre=None, w_post=None
     bt = b.dtype if b is not None else (dh.dtype if dh is not None else r.dtype)
     mode, gp, ldg = _gate(gate, T, H, bt)
     f32 = dict(dtype=torch.float32, device=dev)
-    dx = torch.empty(T, H, dtype=r.dtype, device=dev) if dx is None else dx
+    dx = _empty(stream, T, H, dtype=r.dtype, device=dev) if dx is None else dx
     if b is not None:
-        db = torch.empty(T, H, dtype=bt, device=dev) if db is None else db
+        db = _empty(stream, T, H, dtype=bt, device=dev) if db is None else db
         if w_post is not None and dw_post is None:
-            dw_post = torch.empty(H, **f32)
+            dw_post = _empty(stream, H, **f32)
         if mode == MOE_GATE_FULL:
-            dgate = torch.empty(T, H, dtype=bt, device=dev) if dgate is None else dgate
+            dgate = _empty(stream, T, H, dtype=bt, device=dev) if dgate is None else dgate
         elif mode != MOE_GATE_NONE:
-            dgate = torch.empty(gate.shape, **f32) if dgate is None else dgate
+            dgate = _empty(stream, *gate.shape, **f32) if dgate is None else dgate
     elif gate is not None or w_post is not None:
         raise ValueError("gate and w_post belong to a block output b")
     if dh is not None and w_pre is None:
         raise ValueError("dh needs w_pre")
     if dh is not None and dw_pre is None:
-        dw_pre = torch.empty(H, **f32)
+        dw_pre = _empty(stream, H, **f32)
     if ws is None:
-        ws = torch.empty(max(moe_block_norm_backward_workspace_bytes(T, H), 16), dtype=torch.uint8,
-                         device=dev)
+        ws = _empty(stream, max(moe_block_norm_backward_workspace_bytes(T, H), 16),
+                    dtype=torch.uint8, device=dev)
     if mode == MOE_GATE_FULL:
         dgp, lddg = _rows(dgate, T, H, bt, "dgate")
     else:
@@ -711,7 +727,7 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
     if group_offsets.numel() != G + 1:
         raise ValueError(f"group_offsets: need {G + 1} values")
     if out is None:
-        out = torch.empty(total_rows, n, dtype=out_dtype, device=a.device)
+        out = _empty(stream, total_rows, n, dtype=out_dtype, device=a.device)
     ap, lda = _rows(a, a.shape[0], K, torch.bfloat16, "a")
     op, ldo = _rows(out, total_rows, n, out.dtype, "out")
     args = GemmBf16Args(ap, lda, a.shape[0],
@@ -721,7 +737,7 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
                         _vector(row_scale, total_rows, "row_scale"))
     need = moe_grouped_gemm_bf16_workspace_bytes(G, total_rows, n, K)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=a.device)
     _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(
         ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _queue(stream)))
     return out
@@ -744,7 +760,7 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty(G, n, k, dtype=out_dtype, device=a.device)
+        out = _empty(stream, G, n, k, dtype=out_dtype, device=a.device)
     if tuple(out.shape) != (G, n, k):
         raise ValueError(f"out: need [{G}, {n}, {k}], got {tuple(out.shape)}")
     _dev(out, out.dtype, "out")
@@ -752,7 +768,7 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
     bp, ldb = _rows(b, b.shape[0], k, torch.bfloat16, "b")
     need = moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=a.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=a.device)
     args = WgradBf16Args(ap, lda, a.shape[0],
                          _vector(a_row_index, total_rows, "a_row_index", torch.int32),
                          bp, ldb, b.shape[0],
@@ -769,7 +785,7 @@ def moe_swiglu(a, h=None, stream=None):
     R, I = a.shape[0], a.shape[1] // 2
     if a.shape[1] % 2:
         raise ValueError("a: need an even number of columns (gate columns, then up columns)")
-    h = torch.empty(R, I, dtype=a.dtype, device=a.device) if h is None else h
+    h = _empty(stream, R, I, dtype=a.dtype, device=a.device) if h is None else h
     ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
     hp, ldh = _rows(h, R, I, a.dtype, "h")
     _check("moe_swiglu", lib().moe_swiglu(ap, _dtype_code(a, "a"), R, I, lda, hp, ldh,
@@ -785,9 +801,9 @@ def moe_swiglu_backward(a, dh, row_gate=None, da=None, dgate=None, hg=None, stre
     result that is not wanted."""
     R, I = dh.shape
     dt = _dtype_code(a, "a")
-    da = torch.empty(R, 2 * I, dtype=a.dtype, device=a.device) if da is None else da
-    dgate = torch.empty(R, dtype=torch.float32, device=a.device) if dgate is None else dgate
-    hg = torch.empty(R, I, dtype=a.dtype, device=a.device) if hg is None else hg
+    da = _empty(stream, R, 2 * I, dtype=a.dtype, device=a.device) if da is None else da
+    dgate = _empty(stream, R, dtype=torch.float32, device=a.device) if dgate is None else dgate
+    hg = _empty(stream, R, I, dtype=a.dtype, device=a.device) if hg is None else hg
     dgate, hg = (None if t is False else t for t in (dgate, hg))
     ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
     dhp, lddh = _rows(dh, R, I, a.dtype, "dh")
@@ -855,8 +871,8 @@ class GradList:
 def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
     """Global 2-norm of a GradList's gradients.  Returns (sumsq float64 [1],
     norm float32 [1]), both on the device."""
-    sumsq = torch.empty(1, dtype=torch.float64, device=grads.device) if sumsq is None else sumsq
-    norm = torch.empty(1, dtype=torch.float32, device=grads.device) if norm is None else norm
+    sumsq = _empty(stream, 1, dtype=torch.float64, device=grads.device) if sumsq is None else sumsq
+    norm = _empty(stream, 1, dtype=torch.float32, device=grads.device) if norm is None else norm
     _check("moe_grad_norm", lib().moe_grad_norm(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
         _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), _queue(stream)))
@@ -866,7 +882,8 @@ def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
 def moe_grad_scale(grads, sumsq, max_norm, result=None, stream=None):
     """The scaling of moe_grad_clip from a given sum of squares (float64 [1],
     for instance summed over ranks).  Returns result float32 [2] (norm, coef)."""
-    result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
+    result = _empty(stream, 2, dtype=torch.float32, device=grads.device) \
+        if result is None else result
     _check("moe_grad_scale", lib().moe_grad_scale(
         _ptr(grads.table), grads.n, grads.chunks, _vector(sumsq, 1, "sumsq", torch.float64),
         float(max_norm), _vector(result, 2, "result"), _queue(stream)))
@@ -877,7 +894,8 @@ def moe_grad_clip(grads, max_norm, result=None, stream=None):
     """Clip a GradList to max_norm: outs = coef * gradients, coef = min(1,
     max_norm / (norm + 1e-6)), or 1 when the norm is not finite.  Returns
     result float32 [2] on the device: (norm, coef)."""
-    result = torch.empty(2, dtype=torch.float32, device=grads.device) if result is None else result
+    result = _empty(stream, 2, dtype=torch.float32, device=grads.device) \
+        if result is None else result
     _check("moe_grad_clip", lib().moe_grad_clip(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
         float(max_norm), _vector(result, 2, "result"), _queue(stream)))
