@@ -834,7 +834,8 @@ class GradList:
     dense).  outs: where the clipped gradients go, tensors of the same sizes
     and strides (None: in place).  Built once; valid while the tensors keep
     their memory, which this object holds on to.  Calls on one list share its
-    scratch: order them on one stream."""
+    scratch: order them on one stream.  The list may be dropped before a call
+    on it has run."""
 
     def __init__(self, tensors, outs=None):
         tensors = list(tensors)
@@ -855,6 +856,7 @@ class GradList:
                                                                         and d.is_contiguous())):
                 raise ValueError(f"outs[{i}]: need the gradient's shape and strides")
         self.tensors, self.outs, self.device = tensors, outs, dev
+        self.home = _queue(None)        # the stream that table and ws belong to
         n = self.n = len(tensors)
         rows = (GradTensor * n)(*[GradTensor(s.data_ptr(), d.data_ptr(), s.numel(), _DT[s.dtype],
                                              _DT[d.dtype]) for s, d in zip(tensors, outs)])
@@ -867,6 +869,16 @@ class GradList:
         self.ws = torch.empty(lib().moe_grad_norm_workspace_bytes(self.chunks), dtype=torch.uint8,
                               device=dev)
 
+    def _queue(self, stream):
+        """The handle of a call's stream, noted with the memory that the caller
+        does not see when it is not the stream which that memory belongs to."""
+        queue = _queue(stream)
+        if queue != self.home:
+            stream = torch.cuda.current_stream() if stream is None else stream
+            self.table.record_stream(stream)
+            self.ws.record_stream(stream)
+        return queue
+
 
 def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
     """Global 2-norm of a GradList's gradients.  Returns (sumsq float64 [1],
@@ -875,7 +887,7 @@ def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
     norm = _empty(stream, 1, dtype=torch.float32, device=grads.device) if norm is None else norm
     _check("moe_grad_norm", lib().moe_grad_norm(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
-        _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), _queue(stream)))
+        _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), grads._queue(stream)))
     return sumsq, norm
 
 
@@ -886,7 +898,7 @@ def moe_grad_scale(grads, sumsq, max_norm, result=None, stream=None):
         if result is None else result
     _check("moe_grad_scale", lib().moe_grad_scale(
         _ptr(grads.table), grads.n, grads.chunks, _vector(sumsq, 1, "sumsq", torch.float64),
-        float(max_norm), _vector(result, 2, "result"), _queue(stream)))
+        float(max_norm), _vector(result, 2, "result"), grads._queue(stream)))
     return result
 
 
@@ -898,7 +910,7 @@ def moe_grad_clip(grads, max_norm, result=None, stream=None):
         if result is None else result
     _check("moe_grad_clip", lib().moe_grad_clip(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
-        float(max_norm), _vector(result, 2, "result"), _queue(stream)))
+        float(max_norm), _vector(result, 2, "result"), grads._queue(stream)))
     return result
 
 

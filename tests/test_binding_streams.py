@@ -26,7 +26,8 @@ class Device(torch.Tensor):
 
 
 class Stream:
-    cuda_stream = 77
+    def __init__(self):
+        self.cuda_stream = id(self)
 
 
 class Library:
@@ -146,3 +147,29 @@ def test_memory_of_a_call_without_a_stream_is_the_current_streams(world, name):
     home, made = world
     CALLS[name](None)
     assert made and all(s is home and t.users is None for s, t in made)
+
+
+@pytest.mark.parametrize("name", ["moe_grad_norm", "moe_grad_scale", "moe_grad_clip"])
+def test_a_list_dropped_behind_a_call_keeps_its_table_until_the_call_has_run(world, monkeypatch, name):
+    home, made = world
+    lists = []
+    make_list = moe.GradList.__init__
+
+    def note(self, *a):
+        make_list(self, *a)
+        self.table, self.ws = (t.as_subclass(Device) for t in (self.table, self.ws))
+        lists.append(self)
+
+    monkeypatch.setattr(moe.GradList, "__init__", note)
+    stream = Stream()
+    CALLS[name](stream)
+    CALLS[name](None)
+    CALLS[name](home)
+    other, own, named = lists
+    for held in ("table", "ws"):
+        assert getattr(other, held).users == [stream]
+        assert getattr(own, held).users is None and getattr(named, held).users is None
+    monkeypatch.setattr(moe, "GradList", lambda tensors: own)
+    with torch.cuda.stream(stream):     # the current stream of the call, not of the list
+        CALLS[name](None)
+    assert own.table.users == own.ws.users == [stream]

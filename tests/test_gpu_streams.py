@@ -72,3 +72,25 @@ def test_scratch_of_a_call_on_another_stream(moe, make):
     for x, y in zip(got, want):
         assert torch.equal(x, y)
     assert all(bool((h == 255).all()) for h in held)
+
+
+def test_list_dropped_behind_a_call_on_another_stream(moe):
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    grads = [_normal(gen, n, dtype=torch.float32) for n in (5, 4096, 100001, 1, 30000)]
+    outs = [torch.empty_like(g) for g in grads]
+    want = moe.moe_grad_clip(moe.GradList(grads, outs), 0.5).clone()
+    kept = [o.clone() for o in outs]
+    for o in outs:
+        o.zero_()
+    busy = _normal(gen, 4096, 4096)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    log("moe_grad_clip of a list that is dropped, on another stream")
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            busy @ busy
+    got = moe.moe_grad_clip(moe.GradList(grads, outs), 0.5, stream=s)
+    held = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (200, 512) for _ in range(8)]
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want) and all(torch.equal(o, k) for o, k in zip(outs, kept))
+    assert all(bool((h == 255).all()) for h in held)
