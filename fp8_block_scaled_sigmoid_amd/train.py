@@ -36,6 +36,15 @@ class BlockWeights:
             raise ValueError("w1 and w2: need [N+1, 2I, H] and [N+1, H, I]")
 
 
+def router_gradient(dgate, gates, s):
+    """Gradient of the picked logits z from that of the gates g = s / sum s over
+    a token's picks, s = sigmoid(z): dz_i = g_i (1 - s_i) (dg_i - sum_j dg_j g_j),
+    without a division, so that tiny scores lose nothing.  Where all scores are
+    zero the router gives 1/k whatever z is, and dz is zero.  All float32 [T,k]."""
+    dz = gates * (1.0 - s) * (dgate - (dgate * gates).sum(1, keepdim=True))
+    return torch.where(s.sum(1, keepdim=True) > 0.0, dz, torch.zeros_like(dz))
+
+
 class MoEBlock:
     """r = alpha x + beta gate rmsnorm(experts(rmsnorm(x, w_pre)), w_post)."""
 
@@ -88,12 +97,10 @@ class MoEBlock:
         moe_grouped_wgrad_bf16(db, act, offsets, R, a_row_index=token_of, out=g["w2"])
         moe_grouped_wgrad_bf16(da, h, offsets, R, b_row_index=token_of, out=g["w1"])
         drows = moe_grouped_gemm_bf16(da, w.w1, offsets, R, b_kn=True)
-        # gates g = s / sum s over a token's picks, s = sigmoid(z)
         picked = idx.long()
-        s = scores.gather(1, picked)
-        dgate = drow[slots].view(T, self.k)
-        ds = (dgate - (dgate * gates).sum(1, keepdim=True)) / s.sum(1, keepdim=True)
-        dz = torch.zeros_like(scores).scatter_(1, picked, ds * s * (1.0 - s)).bfloat16()
+        dpicked = router_gradient(drow[slots].view(T, self.k), gates, scores.gather(1, picked))
+        # bf16, as an operand of the products below
+        dz = torch.zeros_like(scores).scatter_(1, picked, dpicked).bfloat16()
         whole = torch.arange(2, dtype=torch.int32, device=x.device) * T     # one group
         moe_grouped_wgrad_bf16(dz, h, whole, T, out=g["w_router"].unsqueeze(0))
         through_router = moe_grouped_gemm_bf16(dz, w.w_router.unsqueeze(0), whole, T, b_kn=True)
