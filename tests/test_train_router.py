@@ -61,7 +61,7 @@ def test_block_gradients_with_a_token_that_no_expert_scores():
         return torch.empty(*shape, device="cuda").normal_(0, std, generator=gen).to(dtype)
 
     bf = torch.bfloat16
-    router = (normal(N, H, std=0.3) - 2.0).to(bf)
+    router = (normal(N, H, std=0.3) - 1.0).to(bf)
     w = BlockWeights(router, normal(N, std=0.05), normal(N + 1, 2 * I, H, std=0.15, dtype=bf),
                      normal(N + 1, H, I, std=0.2, dtype=bf), torch.ones(H, device="cuda"),
                      torch.ones(H, device="cuda"), normal(H))
