@@ -15,10 +15,13 @@ namespace {
 
 using namespace moe;
 
-// s and silu(g).  exp(-g) overflows to infinity below g = -88.7, where s and
-// silu(g) are 0 to float precision, as they should be.
-__device__ __forceinline__ void sigmoid_silu(float g, float& s, float& silu) {
-  s = 1.0f / (1.0f + expf(-g));
+// s, 1 - s and silu(g), from e = exp(-|g|), which cannot overflow: s is 1 / (1 + e)
+// for g >= 0 and e / (1 + e) below, 1 - s the other one of the two.  silu(g) stays
+// a float down to g = -108, and times a large u it counts.
+__device__ __forceinline__ void sigmoid_silu(float g, float& s, float& rest, float& silu) {
+  const float e = expf(-fabsf(g)), p = 1.0f / (1.0f + e), q = e * p;
+  s = g >= 0.0f ? p : q;
+  rest = g >= 0.0f ? q : p;
   silu = g * s;
 }
 
@@ -37,8 +40,8 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const E* a, long long lda, 
   gv.get(g), uv.get(u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float s, silu;
-    sigmoid_silu(g[j], s, silu);
+    float s, rest, silu;
+    sigmoid_silu(g[j], s, rest, silu);
     g[j] = silu * u[j];
   }
   Vec8<E>::store(h + row * ldh + c, g, I - c);
@@ -75,12 +78,12 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(BwdParams p) {
       gv.get(g), uv.get(u), dv.get(d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float s, silu;
-        sigmoid_silu(g[j], s, silu);
+        float s, rest, silu;
+        sigmoid_silu(g[j], s, rest, silu);
         const float h = silu * u[j], wd = w * d[j];
         sum = __builtin_fmaf(h, d[j], sum);
         hg[j] = w * h;
-        g[j] = wd * u[j] * __builtin_fmaf(silu, 1.0f - s, s);
+        g[j] = wd * u[j] * __builtin_fmaf(silu, rest, s);
         u[j] = wd * silu;
       }
       E* da = static_cast<E*>(p.da) + row * p.ldda;
