@@ -7,9 +7,18 @@ float32), gradients float32 in buffers that stay where they are, so that one
 ``GradList`` over them serves every step:
 
     block = MoEBlock(weights, k=8)
-    r, saved = block.forward(x)
-    dx = block.backward(saved, dr)                 # fills block.grads
+    r, _, saved = block.forward(x)
+    dx, _ = block.backward(saved, dr)              # fills block.grads
     norm, coef = block.clip(1.0)
+
+In a chain of blocks the boundary between two of them is one pass each way: the
+first one forms the second one's norm, and takes back that norm's gradient.
+
+    r1, h1, s1 = one.forward(x, next_w_pre=two.w.w_pre)
+    r2, _, s2 = two.forward(r1, h=h1)
+    dr1, _, dh1 = two.backward(s2, dr2, through_norm=False)
+    dx, _ = one.backward(s1, dr1, dh_next=dh1, next_w_pre=two.w.w_pre,
+                         dw_next=two.grads["w_pre"])
 """
 import torch
 
@@ -78,16 +87,21 @@ class MoEBlock:
                                    alpha=self.alpha, beta=self.beta, eps=self.eps)
         return r, h_next, (x, h, idx, gates, scores, offsets, row_of, token_of, a, b, r, counts)
 
-    def backward(self, saved, dr, dh_next=None, next_w_pre=None):
+    def backward(self, saved, dr, dh_next=None, next_w_pre=None, dw_next=None, through_norm=True):
         """dr: the gradient of r; dh_next: of h_next, when the forward pass formed
-        it.  Fills self.grads and returns (dx, dw_next): the gradient of x, and
-        of next_w_pre (None without it)."""
+        it and the next block went back with through_norm=False (otherwise dr
+        holds that part already).  Overwrites self.grads and returns (dx,
+        dw_next): the gradient of x, and of next_w_pre (None without dh_next;
+        written to dw_next where that is given).  With through_norm=False, for a
+        block whose h was given, returns (dx, dw_next, dh): the gradients of x
+        and h apart, and self.grads["w_pre"] is left to the block before."""
         w, g = self.w, self.grads
         x, h, idx, gates, scores, offsets, row_of, token_of, a, b, r, _ = saved
         T, R = x.shape[0], token_of.numel()
         dx, db, dw_next, _, _ = moe_block_norm_backward(
             r, dr=dr, dh=dh_next, b=b, w_pre=next_w_pre, w_post=w.w_post, gate=w.gate,
-            alpha=self.alpha, beta=self.beta, eps=self.eps, dw_post=g["w_post"], dgate=g["gate"])
+            alpha=self.alpha, beta=self.beta, eps=self.eps, dw_pre=dw_next, dw_post=g["w_post"],
+            dgate=g["gate"])
         # each expert row's combine gate; the shared expert's rows have none
         slots = row_of.view(-1).long()
         row_gate = torch.ones(R, dtype=torch.float32, device=x.device)
@@ -107,6 +121,8 @@ class MoEBlock:
         # a token's expert rows and what came through the router, summed
         dh = moe_combine(drows, torch.ones_like(gates), row_of, T * self.k,
                          residual=through_router)
+        if not through_norm:
+            return dx, dw_next, dh
         dx, _, _, _, _ = moe_block_norm_backward(x, dr=dx, dh=dh, w_pre=w.w_pre, eps=self.eps,
                                                  dw_pre=g["w_pre"])
         return dx, dw_next
