@@ -63,13 +63,14 @@ __device__ __forceinline__ int find_tensor(const ListParams& p, long long c) {
 }
 
 // calls f(entry, first element, elements) for the stretches of this
-// workgroup's range
+// workgroup's range (which ends with the table's last tensor, if the caller's
+// count of chunks says more)
 template <typename F>
 __device__ __forceinline__ void for_stretches(const ListParams& p, F f) {
   const long long lo = p.chunks * blockIdx.x / gridDim.x, hi = p.chunks * (blockIdx.x + 1) / gridDim.x;
   if (lo >= hi) return;
   long long c = lo;
-  for (int t = find_tensor(p, lo); c < hi; ++t) {
+  for (int t = find_tensor(p, lo); c < hi && t < p.n; ++t) {
     const Entry e = p.table[t];
     const long long own = (e.numel + kChunk - 1) / kChunk;
     const long long end = min(hi, e.first_chunk + own);

@@ -172,3 +172,20 @@ def test_grad_clip_of_a_long_list(moe, mixed, in_place):  # noqa: F811
             assert torch.equal(grads[i], t)
         kind = "bf16" if o.dtype == torch.bfloat16 else "f32"
         _close(o, v * result[1], UB[kind] * np.abs(v * result[1]) + 2.0 ** -134, f"tensor {i}")
+
+
+def test_grad_clip_with_more_chunks_than_the_table_holds(moe):  # noqa: F811
+    """A count of another list: the walk ends at the table's last tensor."""
+    gen = torch.Generator(device="cuda").manual_seed(34)
+    grads = [torch.empty(n, device="cuda").normal_(generator=gen) for n in (7, 5000, 0, 12289)]
+    want = [t.clone() for t in grads]
+    moe.moe_grad_clip(moe.GradList(want), 0.5)
+    for more in (1, 100, 9000):
+        mine = [t.clone() for t in grads]
+        lst = moe.GradList(mine)
+        lst.chunks += more
+        lst.ws = torch.empty(2048 * 8, dtype=torch.uint8, device="cuda")
+        log(f"moe_grad_clip with {more} chunks too many")
+        moe.moe_grad_clip(lst, 0.5)
+        for t, w in zip(mine, want):
+            assert float((t - w).abs().max()) <= 2.0 ** -22 * float(w.abs().max()) if t.numel() else True
