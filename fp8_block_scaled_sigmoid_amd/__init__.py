@@ -195,18 +195,22 @@ def _dev(t, dtype, name):
     return t
 
 
-def _empty(stream, *shape, dtype, device, zeros=False):
-    """Memory of a call on `stream` (None: the current one).  It belongs to
-    that stream: the allocator gives it to later work of that stream only, also
-    where the call drops it with its kernels still to run.  The caller's stream
-    is noted as well, where the caller will read and drop a result."""
-    make = torch.zeros if zeros else torch.empty
+def _allocator(stream, make=None):
+    """torch.empty (or `make`) for a call on `stream`: the memory belongs to
+    that stream, so that the allocator gives it to later work of that stream
+    only, also where the call drops it with its kernels still to run.  The
+    caller's stream is noted as well, where the caller will read and drop a
+    result."""
+    make = make or torch.empty
     if stream is None:
-        return make(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = make(*shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream())
-    return t
+        return make
+
+    def on_stream(*shape, **kw):
+        with torch.cuda.stream(stream):
+            t = make(*shape, **kw)
+        t.record_stream(torch.cuda.current_stream())
+        return t
+    return on_stream
 
 
 # ---------------------------------------------------------------------------
@@ -224,19 +228,20 @@ def moe_route_topk(x, w_router, bias, k, scores=True, idx=None, gate=None, ws=No
     scores float32 [T,N] or None).  ws: optional uint8 device scratch of
     moe_route_workspace_bytes(T, H, N) bytes.  n_groups > 1 turns on the
     group-limited selection (the best topk_groups groups are eligible)."""
+    empty = _allocator(stream)
     T, H = x.shape
     N = w_router.shape[0]
     _dev(x, torch.bfloat16, "x"), _dev(w_router, torch.bfloat16, "w_router")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = _empty(stream, T, N, dtype=torch.float32, device=x.device)
+        scores = empty(T, N, dtype=torch.float32, device=x.device)
     elif scores is False:
         scores = None
-    idx = _empty(stream, T, k, dtype=torch.int32, device=x.device) if idx is None else idx
-    gate = _empty(stream, T, k, dtype=torch.float32, device=x.device) if gate is None else gate
+    idx = empty(T, k, dtype=torch.int32, device=x.device) if idx is None else idx
+    gate = empty(T, k, dtype=torch.float32, device=x.device) if gate is None else gate
     if ws is None:
-        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                    device=x.device)
+        ws = empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                   device=x.device)
     _check("moe_route_topk", lib().moe_route_topk(_ptr(x), _ptr(w_router), _ptr(bias), T, H, N, k,
                                                   n_groups, topk_groups, _ptr(scores), _ptr(idx),
                                                   _ptr(gate), _ptr(ws), ws.numel(), _stream(stream)))
@@ -248,22 +253,23 @@ def moe_route_topk_quant_x(x, w_router, bias, k, x_q=None, x_d=None, scores=True
     """moe_route_topk that also writes the 1x128 FP8 quantisation of x (the
     codes and scales fp8_quant_1x128 gives) from the same read of x.
     Returns (idx, gate, scores, x_q uint8 [T,H], x_d float32 [T,H/128])."""
+    empty = _allocator(stream)
     T, H = x.shape
     N = w_router.shape[0]
     _dev(x, torch.bfloat16, "x"), _dev(w_router, torch.bfloat16, "w_router")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = _empty(stream, T, N, dtype=torch.float32, device=x.device)
+        scores = empty(T, N, dtype=torch.float32, device=x.device)
     elif scores is False:
         scores = None
-    idx = _empty(stream, T, k, dtype=torch.int32, device=x.device) if idx is None else idx
-    gate = _empty(stream, T, k, dtype=torch.float32, device=x.device) if gate is None else gate
-    x_q = _empty(stream, T, H, dtype=torch.uint8, device=x.device) if x_q is None else x_q
-    x_d = _empty(stream, T, H // 128, dtype=torch.float32, device=x.device) if x_d is None else x_d
+    idx = empty(T, k, dtype=torch.int32, device=x.device) if idx is None else idx
+    gate = empty(T, k, dtype=torch.float32, device=x.device) if gate is None else gate
+    x_q = empty(T, H, dtype=torch.uint8, device=x.device) if x_q is None else x_q
+    x_d = empty(T, H // 128, dtype=torch.float32, device=x.device) if x_d is None else x_d
     _dev(x_q, torch.uint8, "x_q"), _dev(x_d, torch.float32, "x_d")
     if ws is None:
-        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                    device=x.device)
+        ws = empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                   device=x.device)
     _check("moe_route_topk_quant_x",
            lib().moe_route_topk_quant_x(_ptr(x), _ptr(w_router), _ptr(bias), T, H, N, k, n_groups,
                                         topk_groups, _ptr(scores), _ptr(idx), _ptr(gate),
@@ -278,20 +284,21 @@ def moe_route_topk_fp8(x_q, x_d, w_router_q, w_router_d, bias, k, scores=True, i
     [T,H/128] (fp8_quant_1x128), w_router_q uint8 [N,H] with w_router_d float32
     [N/128,H/128] (fp8_quant_128x128), bias [N] float32.  Same outputs and
     workspace as moe_route_topk."""
+    empty = _allocator(stream)
     T, H = x_q.shape
     N = w_router_q.shape[-2]
     _dev(x_q, torch.uint8, "x_q"), _dev(x_d, torch.float32, "x_d")
     _dev(w_router_q, torch.uint8, "w_router_q"), _dev(w_router_d, torch.float32, "w_router_d")
     _dev(bias, torch.float32, "bias")
     if scores is True:
-        scores = _empty(stream, T, N, dtype=torch.float32, device=x_q.device)
+        scores = empty(T, N, dtype=torch.float32, device=x_q.device)
     elif scores is False:
         scores = None
-    idx = _empty(stream, T, k, dtype=torch.int32, device=x_q.device) if idx is None else idx
-    gate = _empty(stream, T, k, dtype=torch.float32, device=x_q.device) if gate is None else gate
+    idx = empty(T, k, dtype=torch.int32, device=x_q.device) if idx is None else idx
+    gate = empty(T, k, dtype=torch.float32, device=x_q.device) if gate is None else gate
     if ws is None:
-        ws = _empty(stream, max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
-                    device=x_q.device)
+        ws = empty(max(moe_route_workspace_bytes(T, H, N), 16), dtype=torch.uint8,
+                   device=x_q.device)
     _check("moe_route_topk_fp8",
            lib().moe_route_topk_fp8(_ptr(x_q), _ptr(x_d), _ptr(w_router_q), _ptr(w_router_d),
                                     _ptr(bias), T, H, N, k, n_groups, topk_groups, _ptr(scores),
@@ -302,10 +309,11 @@ def moe_route_topk_fp8(x_q, x_d, w_router_q, w_router_d, bias, k, scores=True, i
 
 def moe_topk_from_scores(scores, bias, k, idx=None, gate=None, n_groups=1, topk_groups=1,
                          stream=None):
+    empty = _allocator(stream)
     T, N = scores.shape
     _dev(scores, torch.float32, "scores"), _dev(bias, torch.float32, "bias")
-    idx = _empty(stream, T, k, dtype=torch.int32, device=scores.device) if idx is None else idx
-    gate = _empty(stream, T, k, dtype=torch.float32, device=scores.device) if gate is None else gate
+    idx = empty(T, k, dtype=torch.int32, device=scores.device) if idx is None else idx
+    gate = empty(T, k, dtype=torch.float32, device=scores.device) if gate is None else gate
     _check("moe_topk_from_scores", lib().moe_topk_from_scores(
         _ptr(scores), _ptr(bias), T, N, k, n_groups, topk_groups, _ptr(idx), _ptr(gate),
         _stream(stream)))
@@ -319,19 +327,20 @@ def moe_permute_workspace_bytes(T, N, k):
 def moe_permute(idx, N, with_shared=True, out=None, ws=None, stream=None):
     """idx int32 [T,k] -> (counts [N], offsets [N+2], row_of [T,k],
     token_of [T*k (+T)]), all int32."""
+    empty = _allocator(stream)
     T, k = idx.shape
     _dev(idx, torch.int32, "idx")
     dev = idx.device
     if out is None:
         R = T * k + (T if with_shared else 0)
-        out = (_empty(stream, N, dtype=torch.int32, device=dev),
-               _empty(stream, N + 2, dtype=torch.int32, device=dev),
-               _empty(stream, T, k, dtype=torch.int32, device=dev),
-               _empty(stream, R, dtype=torch.int32, device=dev))
+        out = (empty(N, dtype=torch.int32, device=dev),
+               empty(N + 2, dtype=torch.int32, device=dev),
+               empty(T, k, dtype=torch.int32, device=dev),
+               empty(R, dtype=torch.int32, device=dev))
     counts, offsets, row_of, token_of = out
     nbytes = moe_permute_workspace_bytes(T, N, k)
     if ws is None:
-        ws = _empty(stream, max(nbytes, 16), dtype=torch.uint8, device=dev)
+        ws = empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
     _check("moe_permute", lib().moe_permute(_ptr(idx), T, N, k, 1 if with_shared else 0,
                                             _ptr(counts), _ptr(offsets), _ptr(row_of),
                                             _ptr(token_of), _ptr(ws), ws.numel(),
@@ -358,12 +367,13 @@ def moe_permute_noalloc(idx, N, with_shared, out, stream=None):
 
 def fp8_quant_1x128(x, q=None, d=None, stream=None):
     """x [rows, cols] bf16 or float32 -> (q uint8 [rows, cols], d float32 [rows, cols/128])."""
+    empty = _allocator(stream)
     rows, cols = x.shape
     dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[x.dtype]
     if x.stride(1) != 1:
         raise ValueError("x: rows must be contiguous")
-    q = _empty(stream, rows, cols, dtype=torch.uint8, device=x.device) if q is None else q
-    d = _empty(stream, rows, cols // 128, dtype=torch.float32, device=x.device) if d is None else d
+    q = empty(rows, cols, dtype=torch.uint8, device=x.device) if q is None else q
+    d = empty(rows, cols // 128, dtype=torch.float32, device=x.device) if d is None else d
     _check("fp8_quant_1x128", lib().fp8_quant_1x128(_ptr(x), dt, rows, cols, x.stride(0), _ptr(q),
                                                     _ptr(d), _stream(stream)))
     return q, d
@@ -371,12 +381,13 @@ def fp8_quant_1x128(x, q=None, d=None, stream=None):
 
 def fp8_quant_128x128(w, interleave_gate_up=False, q=None, d=None, stream=None):
     """w [batch, rows, cols] bf16 -> (q uint8 like w, d float32 [batch, rows/128, cols/128])."""
+    empty = _allocator(stream)
     if w.dim() == 2:
         w = w.unsqueeze(0)
     B, rows, cols = w.shape
     _dev(w, torch.bfloat16, "w")
-    q = _empty(stream, B, rows, cols, dtype=torch.uint8, device=w.device) if q is None else q
-    d = _empty(stream, B, rows // 128, cols // 128, dtype=torch.float32, device=w.device) \
+    q = empty(B, rows, cols, dtype=torch.uint8, device=w.device) if q is None else q
+    d = empty(B, rows // 128, cols // 128, dtype=torch.float32, device=w.device) \
         if d is None else d
     _check("fp8_quant_128x128", lib().fp8_quant_128x128(_ptr(w), B, rows, cols,
                                                         1 if interleave_gate_up else 0, _ptr(q),
@@ -390,16 +401,17 @@ def moe_grouped_gemm_fp8(a_q, a_d, b_q, b_d, group_offsets, total_rows, epilogue
     """Grouped block-scaled FP8 GEMM (see include/moe_fp8.h).  b_q [G, n_out, K].
     tile_rows None calls moe_grouped_gemm_fp8 (the library picks the row tile);
     0, 128 or 256 calls moe_grouped_gemm_fp8_tiles with it."""
+    empty = _allocator(stream)
     G, n_out, K = b_q.shape
     dev = a_q.device
     if out is None:
         if epilogue == MOE_EPI_SWIGLU_FP8:
-            out = _empty(stream, total_rows, n_out // 2, dtype=torch.uint8, device=dev)
-            out_d = _empty(stream, total_rows, n_out // 256, dtype=torch.float32, device=dev)
+            out = empty(total_rows, n_out // 2, dtype=torch.uint8, device=dev)
+            out_d = empty(total_rows, n_out // 256, dtype=torch.float32, device=dev)
         elif epilogue == MOE_EPI_BF16:
-            out = _empty(stream, total_rows, n_out, dtype=torch.bfloat16, device=dev)
+            out = empty(total_rows, n_out, dtype=torch.bfloat16, device=dev)
         else:
-            out = _empty(stream, total_rows, n_out, dtype=torch.float32, device=dev)
+            out = empty(total_rows, n_out, dtype=torch.float32, device=dev)
     args = GemmArgs(a_q.data_ptr(), a_d.data_ptr(), a_q.stride(0), a_q.shape[0],
                     a_row_index.data_ptr() if a_row_index is not None else None,
                     b_q.data_ptr(), b_d.data_ptr(), group_offsets.data_ptr(), G, total_rows,
@@ -418,13 +430,14 @@ def fp8_transpose_128x128(w_q, w_d, wt_q=None, wt_d=None, stream=None):
     """Exact transpose of 128x128 block-quantised weights: w_q uint8
     [B, rows, cols], w_d float32 [B, rows/128, cols/128] -> (wt_q [B, cols,
     rows], wt_d [B, cols/128, rows/128]).  The B operand of Dgrad."""
+    empty = _allocator(stream)
     if w_q.dim() == 2:
         w_q, w_d = w_q.unsqueeze(0), w_d.unsqueeze(0)
     B, rows, cols = w_q.shape
     _dev(w_q, torch.uint8, "w_q"), _dev(w_d, torch.float32, "w_d")
     dev = w_q.device
-    wt_q = _empty(stream, B, cols, rows, dtype=torch.uint8, device=dev) if wt_q is None else wt_q
-    wt_d = _empty(stream, B, cols // 128, rows // 128, dtype=torch.float32, device=dev) \
+    wt_q = empty(B, cols, rows, dtype=torch.uint8, device=dev) if wt_q is None else wt_q
+    wt_d = empty(B, cols // 128, rows // 128, dtype=torch.float32, device=dev) \
         if wt_d is None else wt_d
     _check("fp8_transpose_128x128", lib().fp8_transpose_128x128(
         _ptr(w_q), _ptr(w_d), B, rows, cols, _ptr(wt_q), _ptr(wt_d), _stream(stream)))
@@ -442,6 +455,7 @@ def fp8_quant_tokens_128(x, group_offsets, ldt=None, xt_q=None, xt_d=None, pad_o
     """Token-tile quantiser (Wgrad operands).  x [rows, cols] bf16 or float32
     in expert-grouped row order, group_offsets int32 [G+1] -> (xt_q uint8
     [cols, ldt], xt_d float32 [cols, ldt/128], pad_offsets int32 [G+1])."""
+    empty = _allocator(stream)
     rows, cols = x.shape
     G = group_offsets.numel() - 1
     dt = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}[x.dtype]
@@ -450,10 +464,10 @@ def fp8_quant_tokens_128(x, group_offsets, ldt=None, xt_q=None, xt_d=None, pad_o
     _dev(group_offsets, torch.int32, "group_offsets")
     ldt = tokens_padded_width(rows, G) if ldt is None else ldt
     dev = x.device
-    xt_q = _empty(stream, cols, ldt, dtype=torch.uint8, device=dev) if xt_q is None else xt_q
-    xt_d = _empty(stream, cols, ldt // 128, dtype=torch.float32, device=dev) \
+    xt_q = empty(cols, ldt, dtype=torch.uint8, device=dev) if xt_q is None else xt_q
+    xt_d = empty(cols, ldt // 128, dtype=torch.float32, device=dev) \
         if xt_d is None else xt_d
-    pad_offsets = _empty(stream, G + 1, dtype=torch.int32, device=dev) if pad_offsets is None \
+    pad_offsets = empty(G + 1, dtype=torch.int32, device=dev) if pad_offsets is None \
         else pad_offsets
     _check("fp8_quant_tokens_128", lib().fp8_quant_tokens_128(
         _ptr(x), dt, rows, cols, x.stride(0), _ptr(group_offsets), G, _ptr(xt_q), _ptr(xt_d),
@@ -464,6 +478,7 @@ def fp8_quant_tokens_128(x, group_offsets, ldt=None, xt_q=None, xt_d=None, pad_o
 def moe_grouped_wgrad_fp8(a_q, a_d, b_q, b_d, pad_offsets, out=None, stream=None):
     """Wgrad grouped GEMM: out[g] = dY_g^T X_g (float32 [G, N, K]) from the
     token-tile operands a (dY^T, [N, lda]) and b (X^T, [K, ldb])."""
+    empty = _allocator(stream)
     N, lda = a_q.shape
     K, ldb = b_q.shape
     G = pad_offsets.numel() - 1
@@ -471,7 +486,7 @@ def moe_grouped_wgrad_fp8(a_q, a_d, b_q, b_d, pad_offsets, out=None, stream=None
                      (b_q, torch.uint8, "b_q"), (b_d, torch.float32, "b_d"),
                      (pad_offsets, torch.int32, "pad_offsets")):
         _dev(t, dt, n)
-    out = _empty(stream, G, N, K, dtype=torch.float32, device=a_q.device) if out is None else out
+    out = empty(G, N, K, dtype=torch.float32, device=a_q.device) if out is None else out
     _check("moe_grouped_wgrad_fp8", lib().moe_grouped_wgrad_fp8(
         _ptr(a_q), _ptr(a_d), lda, N, _ptr(b_q), _ptr(b_d), ldb, K, _ptr(pad_offsets), G,
         _ptr(out), _stream(stream)))
@@ -491,9 +506,10 @@ def moe_grouped_dgrad_fp8(dy, wt_q, wt_d, group_offsets, epilogue=MOE_EPI_BF16, 
 
 
 def moe_combine(out_rows, gate, row_of, shared_row0, residual=None, y=None, stream=None):
+    empty = _allocator(stream)
     T, k = row_of.shape
     H = out_rows.shape[1]
-    y = _empty(stream, T, H, dtype=torch.bfloat16, device=out_rows.device) if y is None else y
+    y = empty(T, H, dtype=torch.bfloat16, device=out_rows.device) if y is None else y
     _check("moe_combine", lib().moe_combine(_ptr(out_rows), _ptr(gate), _ptr(row_of), shared_row0,
                                             T, H, k, _ptr(residual), _ptr(y), _stream(stream)))
     return y
@@ -509,11 +525,12 @@ def moe_bias_update(bias, counts, T, k, gamma, stream=None):
 def moe_seq_balance_loss(idx, gate, seq_offsets, n_experts, alpha=1e-4, loss=None, stream=None):
     """Sequence-wise balance statistic per sequence: idx int32 [T,k], gate
     float32 [T,k], seq_offsets int32 [S+1] (device) -> loss float32 [S]."""
+    empty = _allocator(stream)
     T, k = idx.shape
     _dev(idx, torch.int32, "idx"), _dev(gate, torch.float32, "gate")
     _dev(seq_offsets, torch.int32, "seq_offsets")
     S = seq_offsets.numel() - 1
-    loss = _empty(stream, max(S, 0), dtype=torch.float32, device=idx.device) \
+    loss = empty(max(S, 0), dtype=torch.float32, device=idx.device) \
         if loss is None else loss
     _check("moe_seq_balance_loss", lib().moe_seq_balance_loss(
         _ptr(idx), _ptr(gate), _ptr(seq_offsets), S, T, n_experts, k, alpha, _ptr(loss),
@@ -526,7 +543,7 @@ def moe_probe_fp8_mfma(blocks, iters, sink=None, stream=None):
     blocks * 4 waves, each issuing iters * 16 16x16x128 FP8 MFMAs.  Returns
     (sink, flops)."""
     if sink is None:
-        sink = _empty(stream, blocks * 256, dtype=torch.float32, device="cuda")
+        sink = _allocator(stream)(blocks * 256, dtype=torch.float32, device="cuda")
     _check("moe_probe_fp8_mfma", lib().moe_probe_fp8_mfma(blocks, iters, _ptr(sink),
                                                           _stream(stream)))
     return sink, float(blocks) * 4 * iters * 16 * 65536
@@ -538,7 +555,7 @@ def moe_probe_hbm(mode, buf, sink=None, stream=None):
     loads in flight per lane; ordinary, four), modes 1 and 3 write them
     (non-temporal; ordinary stores).  Returns the sink (read modes) or None."""
     if mode in (0, 2) and sink is None:
-        sink = _empty(stream, 1, dtype=torch.int32, device=buf.device, zeros=True)
+        sink = _allocator(stream, torch.zeros)(1, dtype=torch.int32, device=buf.device)
     _check("moe_probe_hbm", lib().moe_probe_hbm(mode, _ptr(buf), buf.numel() * buf.element_size(),
                                                 _ptr(sink), _stream(stream)))
     return sink
@@ -555,15 +572,16 @@ def moe_layer_forward(w, x, k, gamma=1e-3, n_groups=1, topk_groups=1, router_fp8
     MoEWeights, x [T,H] bf16.  Returns y [T,H] bf16.  scores / idx / gate /
     counts: optional device outputs.  ws: optional uint8 device workspace of
     moe_layer_workspace_bytes(...) bytes (allocated here when None)."""
+    empty = _allocator(stream)
     T, H = x.shape
     _dev(x, torch.bfloat16, "x"), _dev(w.bias, torch.float32, "bias")
     with_shared = w.G == w.N + 1
     if router_fp8 and w.w_router_q is None:
         raise ValueError("router_fp8 needs MoEWeights(..., router_fp8=True)")
-    y = _empty(stream, T, H, dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = empty(T, H, dtype=torch.bfloat16, device=x.device) if y is None else y
     if ws is None:
-        ws = _empty(stream, max(moe_layer_workspace_bytes(T, H, w.N, k, w.I, with_shared), 256),
-                    dtype=torch.uint8, device=x.device)
+        ws = empty(max(moe_layer_workspace_bytes(T, H, w.N, k, w.I, with_shared), 256),
+                   dtype=torch.uint8, device=x.device)
     a = LayerArgs(x.data_ptr(), w.w_router.data_ptr(),
                   w.w_router_q.data_ptr() if w.w_router_q is not None else None,
                   w.w_router_d.data_ptr() if w.w_router_d is not None else None,
@@ -638,19 +656,20 @@ def moe_block_norm(x, b=None, w_pre=None, w_post=None, gate=None, alpha=1.0, bet
     w_pre / w_post float32 [H] (None: h is not formed / b is not normalised),
     gate float32 [H] or [T,1], or [T,H] of b's type.  Returns (r, h); h has
     b's type (x's without b) unless an output is given."""
+    empty = _allocator(stream)
     T, H = x.shape
     xdt = _dtype_code(x, "x")
     if b is not None:
         bt = b.dtype
         _dtype_code(b, "b")
-        r = _empty(stream, T, H, dtype=x.dtype, device=x.device) if r is None else r
+        r = empty(T, H, dtype=x.dtype, device=x.device) if r is None else r
     else:
         if gate is not None or w_post is not None:
             raise ValueError("gate and w_post belong to a block output b")
         bt = h.dtype if h is not None else x.dtype
         r = None
     if h is None and w_pre is not None:
-        h = _empty(stream, T, H, dtype=bt, device=x.device)
+        h = empty(T, H, dtype=bt, device=x.device)
     mode, gp, ldg = _gate(gate, T, H, bt)
     a = BlockNormArgs(T, H, xdt, _DT.get(bt, -1), *_rows(x, T, H, x.dtype, "x"),
                       *_rows(b, T, H, bt, "b"), _vector(w_pre, H, "w_pre"),
@@ -671,29 +690,30 @@ def moe_block_norm_backward(r, dr=None, dh=None, b=None, w_pre=None, w_post=None
     dr (r's other use) and dh, either of them None.  Returns (dx, db, dw_pre,
     dw_post, dgate), None where the forward pass had no such input; the
     weights' gradients and those of a [H] or [T,1] gate are float32."""
+    empty = _allocator(stream)
     T, H = r.shape
     dev = r.device
     bt = b.dtype if b is not None else (dh.dtype if dh is not None else r.dtype)
     mode, gp, ldg = _gate(gate, T, H, bt)
     f32 = dict(dtype=torch.float32, device=dev)
-    dx = _empty(stream, T, H, dtype=r.dtype, device=dev) if dx is None else dx
+    dx = empty(T, H, dtype=r.dtype, device=dev) if dx is None else dx
     if b is not None:
-        db = _empty(stream, T, H, dtype=bt, device=dev) if db is None else db
+        db = empty(T, H, dtype=bt, device=dev) if db is None else db
         if w_post is not None and dw_post is None:
-            dw_post = _empty(stream, H, **f32)
+            dw_post = empty(H, **f32)
         if mode == MOE_GATE_FULL:
-            dgate = _empty(stream, T, H, dtype=bt, device=dev) if dgate is None else dgate
+            dgate = empty(T, H, dtype=bt, device=dev) if dgate is None else dgate
         elif mode != MOE_GATE_NONE:
-            dgate = _empty(stream, *gate.shape, **f32) if dgate is None else dgate
+            dgate = empty(*gate.shape, **f32) if dgate is None else dgate
     elif gate is not None or w_post is not None:
         raise ValueError("gate and w_post belong to a block output b")
     if dh is not None and w_pre is None:
         raise ValueError("dh needs w_pre")
     if dh is not None and dw_pre is None:
-        dw_pre = _empty(stream, H, **f32)
+        dw_pre = empty(H, **f32)
     if ws is None:
-        ws = _empty(stream, max(moe_block_norm_backward_workspace_bytes(T, H), 16),
-                    dtype=torch.uint8, device=dev)
+        ws = empty(max(moe_block_norm_backward_workspace_bytes(T, H), 16),
+                   dtype=torch.uint8, device=dev)
     if mode == MOE_GATE_FULL:
         dgp, lddg = _rows(dgate, T, H, bt, "dgate")
     else:
@@ -721,13 +741,14 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
     [G, K, n_out] (the input gradient, from the forward product's weights).
     a bf16 [rows, K] (rows contiguous), group_offsets int32 [G+1] on the
     device.  Returns out [total_rows, n_out] bf16 or float32."""
+    empty = _allocator(stream)
     G = b.shape[0]
     K, n = (b.shape[1], b.shape[2]) if b_kn else (b.shape[2], b.shape[1])
     _dev(b, torch.bfloat16, "b"), _dev(group_offsets, torch.int32, "group_offsets")
     if group_offsets.numel() != G + 1:
         raise ValueError(f"group_offsets: need {G + 1} values")
     if out is None:
-        out = _empty(stream, total_rows, n, dtype=out_dtype, device=a.device)
+        out = empty(total_rows, n, dtype=out_dtype, device=a.device)
     ap, lda = _rows(a, a.shape[0], K, torch.bfloat16, "a")
     op, ldo = _rows(out, total_rows, n, out.dtype, "out")
     args = GemmBf16Args(ap, lda, a.shape[0],
@@ -737,7 +758,7 @@ def moe_grouped_gemm_bf16(a, b, group_offsets, total_rows, b_kn=False, a_row_ind
                         _vector(row_scale, total_rows, "row_scale"))
     need = moe_grouped_gemm_bf16_workspace_bytes(G, total_rows, n, K)
     if ws is None and need:
-        ws = _empty(stream, need, dtype=torch.uint8, device=a.device)
+        ws = empty(need, dtype=torch.uint8, device=a.device)
     _check("moe_grouped_gemm_bf16", lib().moe_grouped_gemm_bf16(
         ctypes.byref(args), _ptr(ws), ws.numel() if ws is not None else 0, _queue(stream)))
     return out
@@ -754,13 +775,14 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
     [rows, n] (the output channels' gradient), b bf16 [rows, k] (the product's
     input), each optionally gathered by its row index.  With accumulate it is
     added to out.  Returns out [G, n, k] float32 or bf16."""
+    empty = _allocator(stream)
     n, k = a.shape[1], b.shape[1]
     _dev(group_offsets, torch.int32, "group_offsets")
     G = group_offsets.numel() - 1
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty(stream, G, n, k, dtype=out_dtype, device=a.device)
+        out = empty(G, n, k, dtype=out_dtype, device=a.device)
     if tuple(out.shape) != (G, n, k):
         raise ValueError(f"out: need [{G}, {n}, {k}], got {tuple(out.shape)}")
     _dev(out, out.dtype, "out")
@@ -768,7 +790,7 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
     bp, ldb = _rows(b, b.shape[0], k, torch.bfloat16, "b")
     need = moe_grouped_wgrad_bf16_workspace_bytes(G, total_rows, n, k)
     if ws is None and need:
-        ws = _empty(stream, need, dtype=torch.uint8, device=a.device)
+        ws = empty(need, dtype=torch.uint8, device=a.device)
     args = WgradBf16Args(ap, lda, a.shape[0],
                          _vector(a_row_index, total_rows, "a_row_index", torch.int32),
                          bp, ldb, b.shape[0],
@@ -782,10 +804,11 @@ def moe_grouped_wgrad_bf16(a, b, group_offsets, total_rows, a_row_index=None, b_
 
 def moe_swiglu(a, h=None, stream=None):
     """h = silu(a[:, :I]) * a[:, I:] for rows a [R, 2I], bf16 or float32."""
+    empty = _allocator(stream)
     R, I = a.shape[0], a.shape[1] // 2
     if a.shape[1] % 2:
         raise ValueError("a: need an even number of columns (gate columns, then up columns)")
-    h = _empty(stream, R, I, dtype=a.dtype, device=a.device) if h is None else h
+    h = empty(R, I, dtype=a.dtype, device=a.device) if h is None else h
     ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
     hp, ldh = _rows(h, R, I, a.dtype, "h")
     _check("moe_swiglu", lib().moe_swiglu(ap, _dtype_code(a, "a"), R, I, lda, hp, ldh,
@@ -799,11 +822,12 @@ def moe_swiglu_backward(a, dh, row_gate=None, da=None, dgate=None, hg=None, stre
     Returns (da [R, 2I], dgate float32 [R], hg [R, I] = row_gate * swiglu(a),
     the second weight gradient's operand); pass dgate=False or hg=False for a
     result that is not wanted."""
+    empty = _allocator(stream)
     R, I = dh.shape
     dt = _dtype_code(a, "a")
-    da = _empty(stream, R, 2 * I, dtype=a.dtype, device=a.device) if da is None else da
-    dgate = _empty(stream, R, dtype=torch.float32, device=a.device) if dgate is None else dgate
-    hg = _empty(stream, R, I, dtype=a.dtype, device=a.device) if hg is None else hg
+    da = empty(R, 2 * I, dtype=a.dtype, device=a.device) if da is None else da
+    dgate = empty(R, dtype=torch.float32, device=a.device) if dgate is None else dgate
+    hg = empty(R, I, dtype=a.dtype, device=a.device) if hg is None else hg
     dgate, hg = (None if t is False else t for t in (dgate, hg))
     ap, lda = _rows(a, R, 2 * I, a.dtype, "a")
     dhp, lddh = _rows(dh, R, I, a.dtype, "dh")
@@ -883,8 +907,9 @@ class GradList:
 def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
     """Global 2-norm of a GradList's gradients.  Returns (sumsq float64 [1],
     norm float32 [1]), both on the device."""
-    sumsq = _empty(stream, 1, dtype=torch.float64, device=grads.device) if sumsq is None else sumsq
-    norm = _empty(stream, 1, dtype=torch.float32, device=grads.device) if norm is None else norm
+    empty = _allocator(stream)
+    sumsq = empty(1, dtype=torch.float64, device=grads.device) if sumsq is None else sumsq
+    norm = empty(1, dtype=torch.float32, device=grads.device) if norm is None else norm
     _check("moe_grad_norm", lib().moe_grad_norm(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
         _vector(sumsq, 1, "sumsq", torch.float64), _vector(norm, 1, "norm"), grads._queue(stream)))
@@ -894,7 +919,8 @@ def moe_grad_norm(grads, sumsq=None, norm=None, stream=None):
 def moe_grad_scale(grads, sumsq, max_norm, result=None, stream=None):
     """The scaling of moe_grad_clip from a given sum of squares (float64 [1],
     for instance summed over ranks).  Returns result float32 [2] (norm, coef)."""
-    result = _empty(stream, 2, dtype=torch.float32, device=grads.device) \
+    empty = _allocator(stream)
+    result = empty(2, dtype=torch.float32, device=grads.device) \
         if result is None else result
     _check("moe_grad_scale", lib().moe_grad_scale(
         _ptr(grads.table), grads.n, grads.chunks, _vector(sumsq, 1, "sumsq", torch.float64),
@@ -906,7 +932,8 @@ def moe_grad_clip(grads, max_norm, result=None, stream=None):
     """Clip a GradList to max_norm: outs = coef * gradients, coef = min(1,
     max_norm / (norm + 1e-6)), or 1 when the norm is not finite.  Returns
     result float32 [2] on the device: (norm, coef)."""
-    result = _empty(stream, 2, dtype=torch.float32, device=grads.device) \
+    empty = _allocator(stream)
+    result = empty(2, dtype=torch.float32, device=grads.device) \
         if result is None else result
     _check("moe_grad_clip", lib().moe_grad_clip(
         _ptr(grads.table), grads.n, grads.chunks, _ptr(grads.ws), grads.ws.numel(),
