@@ -43,17 +43,14 @@
 // for the long one.  144 rows over 33 groups: 320 to 330 us, 5.9 TB/s of weights.
 #include <type_traits>
 
-#include "common.h"
+#include "rows.h"
 
 namespace {
 
 using namespace moe;
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef const __attribute__((address_space(4))) int32_t* uniform_int_t;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4_t;
@@ -984,7 +981,6 @@ int places() {
   return cus < kXcds ? 32 : cus / kXcds;
 }
 
-bool valid_dt(moe_dtype_t d) { return d == MOE_BF16 || d == MOE_F32; }
 // element rows that 32-bit byte offsets of a gathered operand can reach
 bool fits31(long long rows, long long ld) { return rows * ld * 2 < (1LL << 31); }
 // a tile's or a step's rows of an operand that is not gathered
@@ -1008,7 +1004,7 @@ extern "C" moe_status_t moe_grouped_gemm_bf16(const moe_gemm_bf16_args* args, vo
   if (a.total_rows < 0 || a.n_out < 0 || a.k_dim < 0 || a.n_out % 8 || a.k_dim % 8 ||
       a.num_groups < 1 || a.lda < a.k_dim || a.lda % 8 || a.ldo < a.n_out || a.ldo % 8 || a.a_rows < 0)
     return MOE_ERR_SHAPE;
-  if (a.num_groups > kMaxGroups || !valid_dt(a.out_dtype) ||
+  if (a.num_groups > kMaxGroups || !valid_dtype(a.out_dtype) ||
       (a.b_layout != MOE_B_NK && a.b_layout != MOE_B_KN) ||
       !fits31(a.n_out, a.k_dim) || !tile_fits31(a.lda) ||
       (a.b_layout == MOE_B_KN && !fits31(kStep, a.n_out)))
@@ -1056,7 +1052,7 @@ extern "C" moe_status_t moe_grouped_wgrad_bf16(const moe_wgrad_bf16_args* args, 
   if (a.total_rows < 0 || a.n < 0 || a.k < 0 || a.n % 8 || a.k % 8 || a.num_groups < 1 ||
       a.lda < a.n || a.lda % 8 || a.ldb < a.k || a.ldb % 8 || a.a_rows < 0 || a.b_rows < 0)
     return MOE_ERR_SHAPE;
-  if (a.num_groups > kMaxGroups || !valid_dt(a.out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (a.num_groups > kMaxGroups || !valid_dtype(a.out_dtype)) return MOE_ERR_UNSUPPORTED;
   if ((a.a_row_index && !fits31(a.a_rows, a.lda)) || (a.b_row_index && !fits31(a.b_rows, a.ldb)) ||
       !tile_fits31(a.lda) || !tile_fits31(a.ldb))
     return MOE_ERR_UNSUPPORTED;

@@ -1,6 +1,6 @@
-// Helpers of the row-wise kernels (block norms, gated activation, gradient
-// clipping): bf16 and float rows at any element alignment, eight elements at a
-// time, held as loaded until they are used.
+// Helpers of the training operators: vector types, and for the row-wise kernels
+// (block norms, gated activation, gradient clipping) bf16 and float rows at any
+// element alignment, eight elements at a time, held as loaded until they are used.
 #pragma once
 
 #include "common.h"
