@@ -194,9 +194,11 @@ __global__ __launch_bounds__(kFwdWaves * 64) void block_norm_kernel(FwdParams p)
 // dgate = beta w_post S.  A row's four inputs are read once, the next row's
 // while one is worked on (202 -> 159 us at 8192 x 7168, with the sums by DPP);
 // a gate for each element has no registers left for that (1021 x 2049 in
-// float: 18 us, of which two rows' latency is most).  Rows wider than 8192 do not fit
-// the registers, and read theirs again after the first reduction instead
-// (from L2).  One workgroup per compute unit: 256 partial sums of each channel,
+// float: 18 us; 257 vectors make five waves a row, the fifth with one lane, so a
+// workgroup holds three rows, 85 of the 256 go round a second time, and nothing is in
+// flight for that round).  Rows wider than 8192 do not fit the registers, and read
+// theirs again after the first reduction instead (from L2; 4096 x 16384 in bf16: forward
+// 119 us, 4.5 TB/s, backward 238 us, 3.4).  One workgroup per compute unit: 256 partial sums of each channel,
 // 15 MB at 7168, which the second kernel adds in 5 us.
 struct BwdParams {
   moe_block_norm_bwd_args a;

@@ -34,13 +34,15 @@
 //     given offsets beyond the buffer resource's size and read as zero, so
 //     they never meet the group's data, whatever they hold.
 //
-// Measured, in bf16 with weights of 4096 x 7168: one group of 8192 rows runs at 1450 to
-// 1560 TFLOP/s in all three, as the library's product does.  33 groups
-// of together 16384 rows: forward 805 us (1195 TFLOP/s), input gradient 868 us with uneven
-// groups, bound by the matrix cores (77 and 67 % busy) and, for the groups of
-// 256 rows and fewer, by the weights' stream as well; weight gradient to float
-// 1280 us, bound by its 3.9 GB of stores for the short groups and by the matrix cores
-// for the long one.  144 rows over 33 groups: 320 to 330 us, 5.9 TB/s of weights.
+// Measured, in bf16 with weights of 4096 x 7168, over several cards: one group of 8192
+// rows runs at 1260 to 1350 TFLOP/s forward, 1070 to 1180 for the input gradient and 1330
+// to 1440 for the weight gradient (the library's products of these shapes: 1490 to
+// 1600, 1150 to 1280 and 940 to 980).  33 groups of together 16384 rows: forward 805 to
+// 860 us (1120 to 1195 TFLOP/s), input gradient 868 to 945 us with uneven groups, bound
+// by the matrix cores (75 and 67 % busy) and, for the groups of 256 rows and fewer,
+// by the weights' stream as well; weight gradient to float 1270 to 1310 us, bound by
+// its 3.9 GB of stores for the short groups and by the matrix cores for the long
+// one.  144 rows over 33 groups: 315 to 335 us, 5.9 TB/s of weights.
 #include <type_traits>
 
 #include "rows.h"
@@ -614,7 +616,8 @@ __device__ __forceinline__ int prefix(int v, int* tmp, int& total) {
 // golden-ratio stride over the list: a group with many rows needs the matrix
 // cores and hardly any memory, one with few rows the reverse, and this way
 // every moment has some of both (33 groups of together 16384 rows, even and
-// uneven: 810 and 871 us, in list order 812 and 884).  Runs of 16, 32 and 64 tiles
+// uneven, timed in turn on two cards: in list order 1.0 % and 1.0 to 1.8 % more, 858
+// and 867 us, 933 and 945).  Runs of 16, 32 and 64 tiles
 // take 858, 852 and 840 us and 935, 910 and 909; bands of 2, 4 and 8 row tiles 840,
 // 852 and 853, and 923, 910 and 917 (on a card whose clock was lower).
 //
@@ -973,7 +976,11 @@ long long row_tiles(int num_groups, int total_rows) {
 // Up to 48 rows a group on average the weights' stream decides.  32 groups of
 // 4096 x 7168 take, in the stream kernel and in row tiles: at 2 rows a group 307 and
 // 317 us (317 and 323 in the other layout), at 48 328 and 326 (330, 332), at 96
-// 366 and 344 (372, 342), at 160 775 and 374 (787, 358).
+// 366 and 344 (372, 342), at 160 775 and 374 (787, 358); 33 groups of 48 rows, which do
+// not fill whole rounds of row tiles, 368 and 404 (378, 369).  The host knows the
+// mean alone, and a group of hundreds of rows among small ones is streamed once for
+// each 128 of them: 32 groups of 9 and one of 300 rows take 455 and 386 us (421, 346), 30
+// of 10 and three of 400 rows 500 and 411 (476, 360).
 bool streams_weights(int num_groups, int total_rows) { return total_rows <= 48LL * num_groups; }
 // Workgroups of an XCD: one per compute unit (of the whole chip without a device).
 int places() {
