@@ -94,3 +94,49 @@ def test_list_dropped_behind_a_call_on_another_stream(moe):
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want) and all(torch.equal(o, k) for o, k in zip(outs, kept))
     assert all(bool((h == 255).all()) for h in held)
+
+
+def test_replays_of_a_captured_step(moe):
+    """A graph of the operators, replayed with other inputs and eager work in
+    between: the bits of the eager calls on every replay."""
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    sizes, n, k = [700, 1, 0, 2000, 33, 900], 6144, 136      # the products take tiles from counters
+    R, G, off = sum(sizes), len(sizes), _offsets(sizes)
+    w = _normal(gen, G, n, k)
+    x, x0, dy = _normal(gen, R, k), _normal(gen, R, k), _normal(gen, R, n)
+    gain = _normal(gen, k, dtype=torch.float32)
+    one = _offsets([R])
+    dw = torch.empty(G, n, k, device="cuda")
+    grads = moe.GradList([dw[e] for e in range(G)])
+
+    def step():
+        r, h = moe.moe_block_norm(x0, x, gain, gain, gain)
+        a = moe.moe_grouped_gemm_bf16(h, w, off, R)
+        act = moe.moe_swiglu(a)
+        da, dgate, hg = moe.moe_swiglu_backward(a, dy[:, :n // 2])
+        dh = moe.moe_grouped_gemm_bf16(da, w, off, R, b_kn=True)
+        moe.moe_grouped_wgrad_bf16(da, h, off, R, out=dw)
+        parts = moe.moe_grouped_wgrad_bf16(h, x, one, R)     # cut into parts
+        back = moe.moe_block_norm_backward(r, x0, dh, x, gain, gain, gain)
+        result = moe.moe_grad_clip(grads, 0.5)
+        return [r, h, a, act, da, dgate, hg, dh, parts, *back, result, dw]
+
+    assert moe.moe_grouped_gemm_bf16_workspace_bytes(G, R, n, k) > 0
+    assert moe.moe_grouped_wgrad_bf16_workspace_bytes(1, R, k, k) > 0
+    log("a captured step of the training operators")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(4):
+        x.normal_(generator=gen)
+        x0.normal_(generator=gen)
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        for t, u in zip(got, step()):
+            assert torch.equal(t, u)
