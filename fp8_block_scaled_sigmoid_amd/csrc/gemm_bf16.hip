@@ -40,7 +40,7 @@
 // 1600, 1150 to 1280 and 940 to 980).  33 groups of together 16384 rows: forward 805 to
 // 860 us (1120 to 1195 TFLOP/s), input gradient 868 to 945 us with uneven groups, bound
 // by the matrix cores (75 and 67 % busy) and, for the groups of 256 rows and fewer,
-// by the weights' stream as well; weight gradient to float 1270 to 1310 us, bound by
+// by the weights' stream as well; weight gradient to float 1250 to 1320 us, bound by
 // its 3.9 GB of stores for the short groups and by the matrix cores for the long
 // one.  144 rows over 33 groups: 315 to 335 us, 5.9 TB/s of weights.
 #include <type_traits>
