@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void quant_1x32_kernel(const E* x, uint32
     const int r = (int)(row % (uint32_t)rows), block = r >> 7, half = rows >> 8;
     to += ((block < half ? 2 * block : 2 * (block - half) + 1) - block) * 128;
   }
-  const bool there = c < (cols + 31) / 32 * 32;      // the block holds columns
+  const bool there = (c >> 5) <= ((cols - 1) >> 5);      // the block holds columns
   if (there) *reinterpret_cast<uint32_t*>(q + to * mx_code_bytes(cols) + (c >> 1)) = w;
   if ((lane & 3) == 0)
     e[to * mx_scale_bytes(cols) + mx_scale_at((int)piece * 16 + (lane >> 2))] = (uint8_t)(there ? byte : kMxOne);
