@@ -58,6 +58,11 @@ constexpr int kTile = kTileRows;           // rows and columns of a tile
 constexpr int kStepBlocks = 8;             // blocks of 32 columns in a step
 constexpr int kStepBytes = 16 * kStepBlocks;
 constexpr int kHalf = 128 * kStepBytes;    // bytes of a half tile
+// Rows of B from which tiles have more than 128 rows of A: their loads add up to 192 rows to
+// a scalar offset, which may not pass the resource.  At k 7168 a matrix of 192 rows in short
+// tiles and one of 193 in tall ones take 28 and 40 us for 300 rows of A, 32 and 59 for 8192, 81
+// and 82 for 65536, but 68 and 57 for 33 groups of 1024.
+constexpr int kLeastRows = 193;
 // LDS of a tile: [A, B][half][step parity], 32 more rows of A twice, a place for loads
 // that are not wanted, and twice the scales of 256 rows of A and of B and of 64 more of
 // A; or 3 x [A, B0, B1] and twice the scales of 128 rows of A and 256 of B
@@ -74,7 +79,7 @@ struct Operand {
   const uint8_t* base;     // codes
   uint32_t bytes;          // size of the resource
   uint32_t off[2][2];      // [half][j]: this lane's offsets of its two loads of a half tile
-  uint32_t tail;           // added to the offsets in the last step
+  uint32_t tail;           // kOut where the last step has no such block
   uint32_t extra;          // the offset of the load of the extra rows
   uint32_t row_bytes;
 };
@@ -139,10 +144,10 @@ struct Tile {
   }
 
   // The same for rows at one stride (row_bytes), the offset of the first of which is
-  // off[0][0]; rows past the matrix lie past the resource.  The bounds check counts the
-  // scalar offset too and does not wrap where that alone passes the resource (tried on
-  // the device, inside a larger buffer); both offsets together stay below 2^32 because
-  // 288 rows are below 2^31 bytes.
+  // off[0][0]; rows past the matrix lie past the resource.  The bounds check compares a
+  // lane's offset with the resource's bytes less the scalar offset, which is below them: it
+  // is less than kLeastRows rows, and narrower matrices take short tiles.  Both offsets
+  // together stay below 2^32 because 288 rows are below 2^31 bytes.
   template <bool TAIL>
   __device__ __forceinline__ void copy_rows(const Operand& o, int slot, int h, int step) {
     step = min(step, n_steps - 1);
@@ -674,7 +679,8 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_mxfp4_kernel(GemmPar
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr bool kGated = EPI == MOE_EPI_SWIGLU_MXFP4;
   const bool whole = (p.a.k_dim + 31) / 32 % kStepBlocks == 0;
-  TileList<kWidth<kGated>, kThreads> list(groups_of<kGated>(p.a), smem + kLds, smem, p.next, whole ? kMostUnits : kMostUnits - 1);
+  const int most = p.a.n_out < kLeastRows ? 128 / kUnit : whole ? kMostUnits : kMostUnits - 1;
+  TileList<kWidth<kGated>, kThreads> list(groups_of<kGated>(p.a), smem + kLds, smem, p.next, most);
   TileAt t;
   for (int slot = blockIdx.x / kXcds; list.find(slot, t);) {
     const unsigned popped = list.pop();
@@ -710,7 +716,7 @@ bool fits31(long long rows, long long bytes) { return rows == 0 || bytes < (1LL 
 
 // Tiles of either kind of result (a gated one's are half as wide as B's).
 long long tiles_of(int num_groups, int total_rows, int n_out) {
-  return row_tiles(num_groups, total_rows) * ((n_out + 255LL) / 256);
+  return row_tiles(num_groups, total_rows, n_out < kLeastRows ? 128 : kTileRows) * ((n_out + 255LL) / 256);
 }
 
 }  // namespace

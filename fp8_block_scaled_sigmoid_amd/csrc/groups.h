@@ -285,8 +285,8 @@ __device__ __forceinline__ void stream_tiles(const Groups& of, uint8_t* tmp_at, 
 namespace moe {
 
 // Row tiles that the groups can make at most.
-inline long long row_tiles(int num_groups, int total_rows) {
-  return (long long)total_rows / kTileRows + (num_groups < total_rows ? num_groups : total_rows);
+inline long long row_tiles(int num_groups, int total_rows, int tile_rows = kTileRows) {
+  return (long long)total_rows / tile_rows + (num_groups < total_rows ? num_groups : total_rows);
 }
 // Workgroups of an XCD: one per compute unit (of the whole chip without a device).
 inline int places() {
