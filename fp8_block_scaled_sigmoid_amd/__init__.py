@@ -990,6 +990,13 @@ def _here(*tensors):
             raise ValueError(f"need tensors on one device, got {t.device} and {dev}")
 
 
+def _counts(*sizes):
+    """Refuses sizes past the 32 bits of the C entry points, which would take the
+    low ones."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"need sizes below 2^31, got {max(sizes)}")
+
+
 def mxfp4_code_bytes(cols):
     """Bytes of a row of codes: two columns a byte, whole blocks of 32."""
     return (cols + 31) // 32 * 16
@@ -1006,6 +1013,7 @@ def _matrices(x, name):
         raise ValueError(f"{name}: need a device tensor [rows, cols] or [batch, rows, cols], got "
                          f"{tuple(x.shape)} on {x.device}")
     batch, rows, cols = x.shape if x.dim() == 3 else (1, *x.shape)
+    _counts(batch, rows, cols)
     ld = x.stride(-2) if rows > 1 else x.stride(0) if batch > 1 else max(cols, 1)
     if cols > 1 and x.stride(-1) != 1 or ld < cols or batch > 1 and x.stride(0) != rows * ld:
         raise ValueError(f"{name}: need contiguous rows at one stride, got strides {x.stride()}")
@@ -1072,6 +1080,7 @@ def mxfp4_dequant_1x32(q, e, cols=None, out=None, out_dtype=torch.bfloat16, stre
     rows = 1
     for n in lead:
         rows *= n
+    _counts(rows, cols)
     out = empty(*lead, cols, dtype=out_dtype, device=q.device) if out is None else out
     if out.shape != (*lead, cols) or not out.is_contiguous():
         raise ValueError(f"out: need a contiguous tensor {(*lead, cols)}, got {tuple(out.shape)} "
@@ -1112,6 +1121,7 @@ def moe_grouped_gemm_mxfp4(a_q, a_e, b_q, b_e, group_offsets, total_rows, epilog
         raise ValueError(f"b_q: need [G, n_out, bytes], got {tuple(b_q.shape)}")
     G, n, width = b_q.shape
     K = 2 * width if k_dim is None else k_dim
+    _counts(total_rows, a_q.shape[0], n, K)
     cb, sb = mxfp4_code_bytes(K), mxfp4_scale_bytes(K)
     dev = a_q.device
     gated = epilogue == MOE_EPI_SWIGLU_MXFP4
@@ -1203,6 +1213,7 @@ def moe_balance_loss(scores, idx, seq_offsets=None, token_mask=None, alpha=1e-4,
     T, N = scores.shape
     dev, k = scores.device, idx.shape[1]
     S, sp, mp = _sequences(seq_offsets, token_mask, T)
+    _counts(T, N, k, S)
     loss = empty(S, dtype=torch.float32, device=dev) if loss is None else loss
     if stats is None:
         stats = BalanceStats(empty(S, N, dtype=torch.float32, device=dev),
@@ -1241,6 +1252,7 @@ def moe_router_backward(scores, idx, gate=None, dgate=None, load=None, tokens=No
     if load is not None and tokens is None:
         raise ValueError("load needs tokens")
     S, sp, mp = _sequences(seq_offsets, token_mask, T)
+    _counts(T, N, k, S)
     dz = empty(T, N, dtype=out_dtype, device=scores.device) if dz is None else dz
     _here(scores, idx, gate, dgate, load, tokens, seq_offsets, token_mask, dloss, dz)
     sc, lds = _rows(scores, T, N, torch.float32, "scores")
