@@ -49,3 +49,21 @@ def test_one_row_of_almost_2_31_columns(moe, cols):
     del values
     log(f"mxfp4_dequant_1x32 1 x {cols}")
     assert same(moe.mxfp4_dequant_1x32(q, e, cols), want_v, tail_v)
+
+
+@pytest.mark.parametrize("rows", [2 ** 24 - 1, 2 ** 24, 2 ** 24 + 5])
+def test_as_many_pieces_as_one_dimension_of_a_launch_holds(moe, rows):
+    """2^24 pieces of a row: more go on along the launch's second dimension."""
+    period, cols = 1024, 3
+    part, pv = _tensor(_hard(np.random.default_rng(rows % 100), period, cols), "f32")
+    x = part.repeat(-(-rows // period), 1)[:rows]
+    log(f"mxfp4_quant_1x32 {rows} x {cols}")
+    q, e, values = moe.mxfp4_quant_1x32(x, values=True)
+    want_q, want_e, want_v = _want(pv)
+    times = lambda w: torch.from_numpy(w).cuda().repeat(-(-rows // period), 1)[:rows]     # noqa: E731
+    assert torch.equal(q, times(want_q)) and torch.equal(e, times(want_e))
+    log(f"mxfp4_dequant_1x32 {rows} x {cols}")
+    back = moe.mxfp4_dequant_1x32(q, e, cols)
+    want = times(want_v)
+    for got in (values, back):
+        assert torch.equal(got.double().nan_to_num(7e300), want.nan_to_num(7e300))
