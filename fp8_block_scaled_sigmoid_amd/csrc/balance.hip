@@ -25,10 +25,17 @@ using namespace moe;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kLossThreads = 512, kLossWaves = kLossThreads / 64;
+// Tiles: one a compute unit, of at least 16 tokens.  Captured, tiles of 8, 16, 32 and 64 tokens
+// at least take 9.4, 9.1, 9.6 and 10.5 us at 256 x 256, 10.6, 9.7, 9.5 and 10.9 at 512 x 256,
+// and, with fewer slots to add, 16.6, 16.5, 13.0 and 12.4 at 4096 x 256.
 constexpr int kTokens = 16, kMostTokens = 1024;
-constexpr int kTiles = 256;             // one a compute unit
+constexpr int kTiles = 256;
 constexpr int kAtOnce = 4;              // tokens whose scores a wave has in flight
-constexpr int kOneTokens = 64, kOneSequences = 2;      // what one workgroup does by itself
+// What one workgroup does by itself, in one launch.  Captured, it and the two launches take 5.5
+// and 8.5 us at 64 x 64, 7.4 and 8.7 at 128 x 64, 10.8 and 8.8 at 256 x 64; 9.7 and 12.5 at 64 x
+// 1024, 17.0 and 15.0 at 192 x 1024; two sequences, which it takes one after the other, 6.8 and 7.7
+// at 64 x 64 and 12.1 and 12.1 at 64 x 1024, four 9.9 and 7.5.  (Alone the border could be at 128.)
+constexpr int kOneTokens = 64, kOneSequences = 2;
 
 constexpr int kMostSequences = 1 << 23;                // a workgroup of 256 threads each fits a launch
 

@@ -36,7 +36,7 @@
 //
 // Measured, weights of 4096 x 7168, over several cards: one group of 8192 rows takes 132 to
 // 143 us (3370 to 3650 TFLOP/s; the instruction alone, on random operands, reaches 7000 at
-// the clock that its power leaves), 33 groups of together 16384 rows 278 to 290 us
+// the clock that its power leaves), 33 groups of together 16384 rows 275 to 290 us
 // (gated 270 to 275, to float 305 to 312), 32 groups of 256 rows 157 to 163, 144 rows over
 // 33 groups 98 us, 5.2 TB/s of weights.  The matrix cores are busy 41 % of the large
 // call's time.  Per step of 256 columns and tile (from the slope over k): 1.8 us where the
@@ -708,8 +708,10 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_gemm_mxfp4_stream_kernel(
 // and 110, at 64 110 and 115, at 96 125 and 123, at 128 144 and 130, at 160 271 and 135; 33
 // groups of 48 rows, which do not fill whole rounds of row tiles, 114 and 140.  The host
 // knows the mean alone, and a group of hundreds of rows among small ones is
-// streamed once for each 128 of them: 32 groups of 9 and one of 300 rows take 123 and
-// 126 us, 30 of 10 and three of 400 rows 149 and 141.
+// streamed once for each 128 of them: 32 groups of 9 and one of 300 rows take 115 and
+// 136 us or 123 and 126 on another card, 30 of 10 and three of 400 rows 147 and 141, one of 2112
+// among 32 empty ones 70 and 65.  Worst are many groups: of 256, all of 64 rows 901 and 801 us, one
+// of 16129 among single rows 1087 and 920, 32 of 512 among empty ones 541 and 273.
 bool streams_weights(int num_groups, int total_rows) { return total_rows <= 64LL * num_groups; }
 
 bool fits31(long long rows, long long bytes) { return rows == 0 || bytes < (1LL << 31) / rows; }

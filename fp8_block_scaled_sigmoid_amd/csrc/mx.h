@@ -13,7 +13,6 @@ namespace moe {
 constexpr uint32_t kMxOne = 127;      // the scale byte of 2^0
 constexpr uint32_t kMxNan = 255;
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // Bytes of a row of codes, and of scales.

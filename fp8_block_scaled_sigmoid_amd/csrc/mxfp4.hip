@@ -25,8 +25,8 @@ __device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
   return m;
 }
 
-// A launch has fewer than 2^32 threads along a dimension, 2^26 waves: more items go
-// on along y.
+// Items, a wave each, go on along a launch's second dimension from 2^24 on (2^22
+// workgroups, 2^30 threads; a dimension holds fewer than 2^32).
 constexpr uint32_t kMostGroups = 1u << 22;
 __device__ __forceinline__ uint32_t item_of_wave() {
   return (blockIdx.y * kMostGroups + blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);

@@ -81,7 +81,8 @@ class MoEBlock:
         with w_pre by the block before (its next_w_pre), else None.  Returns
         (r, h_next or None, saved): with next_w_pre the next block's norm is
         formed in the same pass as r.  seq_offsets int32 [S+1] and token_mask [T] (on
-        the device; None: one sequence, all tokens) are the balance loss's."""
+        the device; None: one sequence, all tokens) are the balance loss's, and are not
+        read where balance_alpha is 0: without that loss nothing depends on them."""
         w, T = self.w, x.shape[0]
         if h is None:
             h = torch.empty(T, w.H, dtype=torch.bfloat16, device=x.device)
