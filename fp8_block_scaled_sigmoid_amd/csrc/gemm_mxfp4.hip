@@ -146,8 +146,8 @@ struct Tile {
   // The same for rows at one stride (row_bytes), the offset of the first of which is
   // off[0][0]; rows past the matrix lie past the resource.  The bounds check compares a
   // lane's offset with the resource's bytes less the scalar offset, which is below them: it
-  // is less than kLeastRows rows, and narrower matrices take short tiles.  Both offsets
-  // together stay below 2^32 because 288 rows are below 2^31 bytes.
+  // is less than kLeastRows rows, and narrower matrices take short tiles.  A lane's own offset
+  // is less than 64 rows past the matrix, below 2^32 because 288 rows are below 2^31 bytes.
   template <bool TAIL>
   __device__ __forceinline__ void copy_rows(const Operand& o, int slot, int h, int step) {
     step = min(step, n_steps - 1);
